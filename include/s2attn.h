@@ -67,7 +67,9 @@ typedef enum {
 /* Version of this ABI (bumped on any signature change or workspace-size change); 2 adds the
  * dS hand-off entries and the work counters in the backward workspace; 3 adds the option flags
  * (_general entries, which replace the strided-only entries) and s2attn_rope_pi; 4 adds the
- * _general forms of the two dS hand-off stages; 5 adds s2attn_fwd_rope_q. */
+ * _general forms of the two dS hand-off stages; 5 adds s2attn_fwd_rope_q. Entries that were
+ * added beside these without changing any of them (s2attn_rope_append, s2attn_decode) leave the
+ * version as it is: a caller finds out by looking their symbols up. */
 S2ATTN_API int s2attn_abi_version(void);
 
 /* Static description of a status code. */
@@ -309,8 +311,11 @@ S2ATTN_API s2attn_status s2attn_bwd_noalloc(const void* q, const void* k, const 
 /*
  * Synchronises `stream`, then reads and clears the current device's error word.
  * Returns S2ATTN_ERR_TIMEOUT if a kernel gave up on a pipeline wait since the last call
- * (code_out, if not NULL, receives (kernel << 8) | wait site; 0 if none), S2ATTN_ERR_CUDA
- * if the synchronisation failed, S2ATTN_OK otherwise.
+ * (code_out, if not NULL, receives (kernel << 8) | wait site; 0 if none),
+ * S2ATTN_ERR_INVALID_ARG if a serving kernel met an index in the caller's device arrays that
+ * lies outside the cache (s2attn_rope_append, s2attn_decode; code_out as above with site 0x80
+ * for a page number, 0x81 for a length), S2ATTN_ERR_CUDA if the synchronisation failed,
+ * S2ATTN_OK otherwise.
  */
 S2ATTN_API s2attn_status s2attn_get_device_error(void* stream, unsigned int* code_out);
 
@@ -346,6 +351,74 @@ S2ATTN_API s2attn_status s2attn_selftest_wait_timeout(unsigned long long timeout
 S2ATTN_API s2attn_status s2attn_rope_pi(const void* x, void* y, int B, int N, int H, int d,
                                         float base, float pi_scale, int inverse,
                                         const long long* strides, void* stream);
+
+/*
+ * Serving. The fine-tuned model answers with standard attention over the whole extended context
+ * (summary page, §3.2: S²-Attn is used in fine-tuning only), so what follows is full causal
+ * attention with rotary positions and a paged key/value cache:
+ *   s2attn_rope_append  turns new queries and keys and puts keys and values into the cache;
+ *   s2attn_decode       attends from one new token per sequence over the cache.
+ *
+ * Paged cache. k_cache and v_cache are bf16 [pages, page_size, Hkv, d]: pages of page_size >= 1
+ * tokens (any number), handed out to sequences by the caller. block_table is a device array
+ * int32 [B, max_pages]: token t of sequence b is at slot t mod page_size of page
+ * block_table[b][t / page_size]; entries past a sequence's last page are not read. cache_lens is
+ * a device array int32 [B]: tokens of each sequence in the cache, 0 for an idle row of a padded
+ * batch. Both are read on the device, so a captured graph follows them from replay to replay.
+ * A page number outside [0, pages) or a length outside [0, max_pages * page_size] is never
+ * followed: the token is not cached, or counts as zeros, the length is cut to that range, and
+ * s2attn_get_device_error reports it. Cache element (page, slot, h, c) is at page * sp + slot *
+ * st + h * d + c (elements) with sp, st from `strides`, each a multiple of 8, st >= Hkv * d, pages
+ * apart by at least their extent (so K and V may be interleaved in one buffer, by page or by
+ * token); contiguous without. Offsets into the cache are 64-bit.
+ */
+
+/*
+ * Rotation and append. The T new tokens of B sequences are packed row after row: q bf16 [T, Hq,
+ * d], k and v bf16 [T, Hkv, d]; sequence s has rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+ * (device int32 [B + 1], not decreasing; lengths of 0 allowed), or row s alone with cu_seqlens =
+ * NULL (T = B: one new token each). cache_lens[s] counts the sequence's tokens INCLUDING these, so
+ * row i of its n new rows has position cache_lens[s] - n + i. Queries and keys turn by the angle
+ * of that position, pair (x[i], x[i + d/2]) by position * pi_scale * base^(-2i/d) (as
+ * s2attn_rope_pi, but exact to fp32 rounding of sine and cosine at any position); turned queries
+ * go to q_rot, turned keys to the cache and, if not NULL, to k_rot, values to the cache.
+ * q_rot may be q, k_rot may be k; no other overlap. q and q_rot may both be NULL. Rows behind
+ * the last sequence, rows before the first and rows whose position would be negative (idle rows:
+ * cache_lens = 0) are skipped: nothing is written for them. Two tokens must not share a slot.
+ * `strides`: NULL or {q, q_rot, k, k_rot, v row strides, k_cache sp, st, v_cache sp, st}. Row
+ * strides are multiples of 8 and at least heads * d. Errors as above, plus base <= 1, pi_scale <=
+ * 0 -> S2ATTN_ERR_INVALID_ARG; max_pages * page_size > 2^31 - 129 -> S2ATTN_ERR_UNSUPPORTED.
+ * Asynchronous on `stream`; allocates nothing; one launch.
+ */
+S2ATTN_API s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void* k_rot,
+                                            const void* v, void* k_cache, void* v_cache,
+                                            const int* block_table, const int* cu_seqlens,
+                                            const int* cache_lens, int T, int B, int Hq, int Hkv,
+                                            int d, int pages, int page_size, int max_pages,
+                                            float base, float pi_scale, const long long* strides,
+                                            void* stream);
+
+/* Device workspace of s2attn_decode (256-byte aligned; contents on entry do not matter): about 20
+ * MB at d = 128 and 16 or more query heads per kv head, proportional to the smaller of that
+ * group and 16. 0 for arguments s2attn_decode would reject. */
+S2ATTN_API size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
+
+/*
+ * One new token per sequence: o[b, h] = softmax(scale * q[b, h] . K) V over the cache_lens[b] tokens
+ * of sequence b (the new token's key and value among them, appended before), q, o bf16 [B, Hq, d],
+ * lse fp32 [B, Hq] (natural log; may be NULL). Query head h reads kv head h / (Hq / Hkv); any
+ * group size. q must be turned already. A sequence of length 0 gives o = 0 and lse = -inf.
+ * Cache rows past a sequence's length are never used, whatever they hold. The same inputs give the
+ * same bits. `strides`: NULL or {q, o batch strides, k_cache sp, st, v_cache sp, st}. Calls that
+ * may run at the same time need a workspace each. Two launches (the second one joins what was
+ * split), asynchronous on `stream`; allocates nothing.
+ */
+S2ATTN_API s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                                       const int* block_table, const int* cache_lens, void* o,
+                                       float* lse, int B, int Hq, int Hkv, int d, int pages,
+                                       int page_size, int max_pages, float scale,
+                                       const long long* strides, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -38,3 +38,10 @@ from ._lib import (  # noqa: F401
     fwd,
     bwd,
 )
+from ._serve import (  # noqa: F401
+    s2attn_rope_append,
+    s2attn_decode,
+    s2attn_decode_workspace_size,
+    rope_append,
+    decode,
+)

@@ -11,7 +11,7 @@ import sys
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SRC = os.path.join(PKG_DIR, "csrc", "s2attn_api.cu")
+SRCS = [os.path.join(PKG_DIR, "csrc", f) for f in ("s2attn_api.cu", "s2serve_api.cu")]
 LIB = os.path.join(PKG_DIR, "libs2attn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -41,7 +41,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
         return LIB
     cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", SRC]
+           "-t", "0",   # the translation units side by side
+           "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *SRCS]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), flush=True)

@@ -1,0 +1,172 @@
+// Rotation and append: the step between the projections and the attention when a model answers.
+// Each new token's query and key heads turn by the rotary angle of its position (Position
+// Interpolation, LongLoRA summary page, §4 "Model setup"), and the turned key and the value go to
+// the token's slot of a paged cache.
+//
+// For position t and i < D/2 the pair (x[i], x[i + D/2]) turns by t * pi_scale * base^(-2i/D).
+// Positions reach 10^5 and more, where an fp32 product is off by 1e-2 rad; the angle is instead
+// formed in turns, as 64-bit fixed point: F_i = frac(pi_scale * base^(-2i/D) / 2 pi) * 2^64 (from
+// the host, rounded once), and t * F_i modulo 2^64 is the exact fraction of a turn (error
+// t * 2^-64). Its upper 32 bits, as a signed number, are sincospif's argument.
+//
+// Memory bound: every element is read once and written once or twice. A block takes 8 tokens, one
+// warp per token: the warp finds the token's sequence (32-way search of cu_seqlens), its slot, and
+// its D/2 angles, shared by all heads through shared memory. A thread then owns one 16-byte chunk
+// of a head's first half and its partner D/2 columns on, for all 8 tokens: 16 loads of 16 bytes in
+// flight a thread, the first ones issued before the slots and angles are known. A grid of few
+// blocks splits the heads over its second axis.
+#pragma once
+
+#include "s2_serve_common.cuh"
+
+namespace s2 {
+
+constexpr int kAppendTokens = 8;
+constexpr int kAppendThreads = 32 * kAppendTokens;
+
+struct AppendParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_rot, *k_rot;          // k_rot null: the turned keys go to the cache only
+  long long q_st, k_st, v_st, qr_st, kr_st;
+  PagedRef kc, vc;
+  const int *table, *cu, *lens;          // cu null: one token per sequence
+  int T, B, Hq, Hkv, pages, page_size, max_pages;
+  unsigned int* err;
+  unsigned long long turn[64];           // F_i
+};
+
+// The sequence that holds token t: the number of i in [1, B] with cu[i] <= t, by a whole warp.
+__device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;                     // the answer lies in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lo + (lane + 1) * step;
+    const bool below = i <= lo + n && cu[i] <= t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
+    lo += cnt * step;
+    n = step == 1 ? 0 : min(step - 1, B - lo);
+  }
+  return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) s2_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kHalf = D / 2;
+  constexpr int kChunks = D / 16;        // work items of a head: a 16-byte chunk and its partner
+  __shared__ float s_cos[kAppendTokens][kHalf], s_sin[kAppendTokens][kHalf];
+  __shared__ long long s_slot_k[kAppendTokens], s_slot_v[kAppendTokens];   // -1: not to be cached
+  __shared__ int s_live[kAppendTokens];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int t0 = blockIdx.x * kAppendTokens;
+  const int items = (p.Hq + 2 * p.Hkv) * kChunks;
+  const int step = gridDim.y * kAppendThreads;
+  int w = blockIdx.y * kAppendThreads + threadIdx.x;
+
+  uint4 lo[kAppendTokens], hi[kAppendTokens];
+  auto load = [&](int item) {
+    const int h = item / kChunks, c = item % kChunks;
+    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+    const __nv_bfloat16* src = is_q ? p.q : is_k ? p.k : p.v;
+    const long long st = is_q ? p.q_st : is_k ? p.k_st : p.v_st;
+    const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+    src += t0 * st + static_cast<long long>(hh) * D + 8 * c;
+#pragma unroll
+    for (int tt = 0; tt < kAppendTokens; ++tt)
+      if (t0 + tt < p.T) {
+        lo[tt] = *reinterpret_cast<const uint4*>(src + tt * st);
+        hi[tt] = *reinterpret_cast<const uint4*>(src + tt * st + kHalf);
+      }
+  };
+  if (w < items) load(w);
+
+  // ---- this warp's token: position, slot, angles ----
+  {
+    const int t = t0 + warp;
+    long long pos = -1;
+    int seq = p.B;
+    if (t < p.T) {
+      if (p.cu) {
+        seq = find_sequence(p.cu, p.B, t);
+        if (seq < p.B && t >= p.cu[seq])
+          pos = static_cast<long long>(p.lens[seq]) - p.cu[seq + 1] + t;
+      } else {
+        seq = t;
+        pos = static_cast<long long>(p.lens[seq]) - 1;
+      }
+    }
+    if (lane == 0) {
+      long long sk = -1, sv = -1;
+      if (pos >= 0) {
+        if (pos >= static_cast<long long>(p.max_pages) * p.page_size) {
+          report_bad_index(p.err, KID_APPEND, kSiteBadLength);
+        } else {
+          const int slot_page = static_cast<int>(pos / p.page_size), at = static_cast<int>(pos % p.page_size);
+          const int page = p.table[static_cast<long long>(seq) * p.max_pages + slot_page];
+          if (page < 0 || page >= p.pages) {
+            report_bad_index(p.err, KID_APPEND, kSiteBadPage);
+          } else {
+            sk = page * p.kc.sp + at * p.kc.st;
+            sv = page * p.vc.sp + at * p.vc.st;
+          }
+        }
+      }
+      s_slot_k[warp] = sk;
+      s_slot_v[warp] = sv;
+      s_live[warp] = pos >= 0;
+    }
+    if (pos >= 0) {
+#pragma unroll
+      for (int i = lane; i < kHalf; i += 32) {
+        const unsigned long long turns = static_cast<unsigned long long>(pos) * p.turn[i];
+        float sv, cv;
+        sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f, &sv, &cv);
+        s_cos[warp][i] = cv;
+        s_sin[warp][i] = sv;
+      }
+    }
+  }
+  __syncthreads();
+
+  for (; w < items; w += step) {
+    if (w >= step) load(w);
+    const int h = w / kChunks, c = w % kChunks;
+    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+    const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+    const long long col = static_cast<long long>(hh) * D + 8 * c;
+#pragma unroll
+    for (int tt = 0; tt < kAppendTokens; ++tt) {
+      if (t0 + tt >= p.T || !s_live[tt]) continue;
+      uint4 olo = lo[tt], ohi = hi[tt];
+      if (is_q || is_k) {
+        const __nv_bfloat162* l2 = reinterpret_cast<const __nv_bfloat162*>(&lo[tt]);
+        const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&hi[tt]);
+        __nv_bfloat162* ol = reinterpret_cast<__nv_bfloat162*>(&olo);
+        __nv_bfloat162* oh = reinterpret_cast<__nv_bfloat162*>(&ohi);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // fp32 rotation, one rounding to bf16
+          const float2 a = __bfloat1622float2(l2[j]), b = __bfloat1622float2(h2[j]);
+          const float2 cs = *reinterpret_cast<const float2*>(&s_cos[tt][8 * c + 2 * j]);
+          const float2 sn = *reinterpret_cast<const float2*>(&s_sin[tt][8 * c + 2 * j]);
+          ol[j] = __floats2bfloat162_rn(a.x * cs.x - b.x * sn.x, a.y * cs.y - b.y * sn.y);
+          oh[j] = __floats2bfloat162_rn(b.x * cs.x + a.x * sn.x, b.y * cs.y + a.y * sn.y);
+        }
+      }
+      auto store = [&](__nv_bfloat16* dst) {
+        *reinterpret_cast<uint4*>(dst) = olo;
+        *reinterpret_cast<uint4*>(dst + kHalf) = ohi;
+      };
+      if (is_q) {
+        store(p.q_rot + (t0 + tt) * p.qr_st + col);
+      } else if (is_k) {
+        if (p.k_rot) store(p.k_rot + (t0 + tt) * p.kr_st + col);
+        if (s_slot_k[tt] >= 0) store(p.kc.p + s_slot_k[tt] + col);
+      } else if (s_slot_v[tt] >= 0) {
+        store(p.vc.p + s_slot_v[tt] + col);
+      }
+    }
+  }
+}
+
+}  // namespace s2

@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "../../include/s2attn.h"
+#include "s2_host.h"
 #include "s2_bwd_dkdv.cuh"
 #include "s2_bwd_dq.cuh"
 #include "s2_bwd_dq_ds.cuh"
@@ -21,22 +22,21 @@
 #include "s2_rope.cuh"
 #include "s2_fwd.cuh"
 #include "s2_fwd_sched.h"
+#include "s2_serve_common.cuh"
 
 namespace {
 
 __device__ unsigned int g_err_word;   // first pipeline-wait failure since the last read
 
 constexpr int kAbiVersion = 5;
-constexpr int kMaxDevices = 64;
+using s2host::aligned16;
+using s2host::cuda_fail;
+using s2host::device_state;
+using s2host::kMaxDevices;
 constexpr unsigned long long kDefaultTimeoutNs = 1000000000ull;
 
 std::atomic<unsigned long long> g_timeout_ns{kDefaultTimeoutNs};
 thread_local char g_last_error[256] = "";
-
-s2attn_status cuda_fail(cudaError_t e, const char* what) {
-  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, cudaGetErrorString(e));
-  return S2ATTN_ERR_CUDA;
-}
 
 struct DeviceState {
   std::once_flag once;
@@ -77,9 +77,25 @@ cudaError_t set_smem_attrs() {
   return e != cudaSuccess ? e : set_smem_attrs_variant<D, true>();
 }
 
+}  // namespace
+
+namespace s2host {
+
+s2attn_status cuda_fail(cudaError_t e, const char* what) {
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, cudaGetErrorString(e));
+  return S2ATTN_ERR_CUDA;
+}
+
+s2attn_status fail(s2attn_status status, const char* text) {
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s", text);
+  return status;
+}
+
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+
 // Per-device one-time set-up (with that device current): the device address of the error
 // word, and the kernels' shared-memory limits.
-s2attn_status device_state(unsigned int** err_word, int* num_sms = nullptr) {
+s2attn_status device_state(unsigned int** err_word, int* num_sms, int* device) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -101,10 +117,11 @@ s2attn_status device_state(unsigned int** err_word, int* num_sms = nullptr) {
   if (s.init_err != cudaSuccess) return cuda_fail(s.init_err, "device set-up");
   *err_word = s.err_word;
   if (num_sms) *num_sms = s.num_sms;
+  if (device) *device = dev;
   return S2ATTN_OK;
 }
 
-s2attn_status get_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -113,12 +130,15 @@ s2attn_status get_encoder() {
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) {
-    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled unavailable");
-    return S2ATTN_ERR_CUDA;
-  }
-  return S2ATTN_OK;
+  if (!g_encode) fail(S2ATTN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  return g_encode;
 }
+
+}  // namespace s2host
+
+namespace {
+
+s2attn_status get_encoder() { return s2host::encoder() ? S2ATTN_OK : S2ATTN_ERR_CUDA; }
 
 // Tensor map over a bf16 [B, N, H, d] tensor: dims (d, H, N, B), box (64, 1, rows, 1),
 // 128-byte swizzle, zero fill out of bounds.
@@ -148,8 +168,6 @@ s2attn_status encode_pair(MapPair& mp, const void* base, int B, int H, int N, in
   if (s != S2ATTN_OK) return s;
   return encode_map(&mp.m8, base, B, H, N, d, 8, sb, st);
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Workspace layout: D [B, Hq, N] fp32 | LSE2 [B, Hq, N] fp32 | scheduling words | dS tiles.
 // Each array is rounded up to 256 bytes; the scheduling words hold the work counters of the
@@ -903,7 +921,10 @@ s2attn_status s2attn_get_device_error(void* stream, unsigned int* code_out) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   }
   if (code_out) *code_out = code;
-  return code != 0 ? S2ATTN_ERR_TIMEOUT : S2ATTN_OK;
+  if (code == 0) return S2ATTN_OK;
+  const unsigned kernel = code >> 8, site = code & 0xFFu;
+  const bool bad_index = kernel >= s2::KID_APPEND && site >= s2::kSiteBadIndex;
+  return bad_index ? S2ATTN_ERR_INVALID_ARG : S2ATTN_ERR_TIMEOUT;
 }
 
 s2attn_status s2attn_selftest_wait_timeout(unsigned long long timeout_ns, void* stream) {

@@ -1,0 +1,264 @@
+// Host side of the serving entries of the C ABI (rotation and append, decode): argument
+// validation and kernel launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+// s2_device.cuh defines this one function out of line; the library's other translation unit has
+// it under its own name.
+#define wait_slow wait_slow_serve
+
+#include "../../include/s2attn.h"
+#include "s2_append.cuh"
+#include "s2_decode.cuh"
+#include "s2_host.h"
+
+namespace {
+
+using s2host::aligned16;
+using s2host::cuda_fail;
+using s2host::device_state;
+using s2host::kMaxDevices;
+
+struct ServeDevice {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+ServeDevice g_serve_dev[kMaxDevices];
+
+template <int D>
+cudaError_t serve_smem_attrs() {
+  return cudaFuncSetAttribute(s2::s2_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              s2::DecodeLayout<D>::kBytes);
+}
+
+// The error word and SM count of the current device, with the serving kernels set up on it.
+s2attn_status serve_device(unsigned int** err, int* num_sms) {
+  int dev = 0;
+  const s2attn_status s = device_state(err, num_sms, &dev);
+  if (s != S2ATTN_OK) return s;
+  ServeDevice& d = g_serve_dev[dev];
+  std::call_once(d.once, [&] {
+    d.err = serve_smem_attrs<64>();
+    if (d.err == cudaSuccess) d.err = serve_smem_attrs<128>();
+  });
+  return d.err == cudaSuccess ? S2ATTN_OK : cuda_fail(d.err, "device set-up");
+}
+
+s2attn_status check_heads(int Hq, int Hkv, int d) {
+  if (Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return S2ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return S2ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(Hq) * d >= (1ll << 31)) return S2ATTN_ERR_UNSUPPORTED;
+  return S2ATTN_OK;
+}
+
+// A token (or batch row) stride: whole 16-byte chunks, rows that do not overlap.
+bool bad_row_stride(long long st, int heads, int d) {
+  return st % 8 != 0 || st < static_cast<long long>(heads) * d;
+}
+
+// The paged cache's shape and {page, token} strides of K and V (null: contiguous).
+s2attn_status check_cache(int Hkv, int d, int pages, int page_size, int max_pages,
+                          const long long* strides, s2::PagedRef& kc, s2::PagedRef& vc) {
+  if (pages <= 0 || page_size <= 0 || max_pages <= 0) return S2ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * page_size > INT_MAX - 128) return S2ATTN_ERR_UNSUPPORTED;
+  const long long st = static_cast<long long>(Hkv) * d;
+  kc.st = vc.st = st;
+  kc.sp = vc.sp = st * page_size;
+  if (strides) {
+    for (int i = 0; i < 4; i += 2) {
+      const long long sp = strides[i], tt = strides[i + 1];
+      // tokens of a page may interleave with other tensors, pages may not overlap
+      if (bad_row_stride(tt, Hkv, d) || sp % 8 != 0 || sp <= 0) return S2ATTN_ERR_INVALID_ARG;
+      if (pages > 1 && sp < (page_size - 1) * tt + st) return S2ATTN_ERR_INVALID_ARG;
+    }
+    kc.sp = strides[0]; kc.st = strides[1];
+    vc.sp = strides[2]; vc.st = strides[3];
+  }
+  return S2ATTN_OK;
+}
+
+s2::FastDiv fast_div_by(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  s2::FastDiv f;
+  f.shift = 31 + l;
+  f.mul = static_cast<unsigned int>(((1ull << f.shift) + d - 1) / d);
+  return f;
+}
+
+// F_i of s2_append.cuh for one (base, pi_scale, d); the last one is kept by each host thread.
+const unsigned long long* turns(float base, float pi_scale, int d) {
+  static thread_local struct { float base, pi; int d; unsigned long long f[64]; } last = {0.f, 0.f, 0, {}};
+  if (last.base != base || last.pi != pi_scale || last.d != d) {
+    const long double two_pi = 6.283185307179586476925286766559L;
+    for (int i = 0; i < d / 2; ++i) {
+      long double x = static_cast<long double>(pi_scale) *
+                      powl(static_cast<long double>(base), -2.0L * i / d) / two_pi;
+      x = (x - floorl(x)) * 18446744073709551616.0L;
+      last.f[i] = x >= 18446744073709551615.0L ? 0ull : static_cast<unsigned long long>(x + 0.5L);
+    }
+    last.base = base;
+    last.pi = pi_scale;
+    last.d = d;
+  }
+  return last.f;
+}
+
+constexpr size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+// Workspace of the decode: partial outputs | partial {max, sum} | plan.
+struct DecodeSpace {
+  size_t o, ml, plan;
+};
+DecodeSpace decode_space(int B, int group, int d) {
+  const size_t slots = static_cast<size_t>(s2::kDecodeMaxCtas) * s2::kDecodeWarps * 2 *
+                       std::min(group, s2::kDecodeRows);
+  return {round256(slots * d * sizeof(float)), round256(slots * sizeof(float2)),
+          round256((static_cast<size_t>(B) + 1) * sizeof(long long))};
+}
+
+template <int D>
+s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t stream) {
+  s2::s2_decode_kernel<D><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "s2_decode_kernel launch");
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq);
+  cfg.blockDim = dim3(s2::kDecodeJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, s2::s2_decode_join_kernel<D>, p);
+  return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_decode_join_kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void* k_rot,
+                                 const void* v, void* k_cache, void* v_cache,
+                                 const int* block_table, const int* cu_seqlens,
+                                 const int* cache_lens, int T, int B, int Hq, int Hkv, int d,
+                                 int pages, int page_size, int max_pages, float base,
+                                 float pi_scale, const long long* strides, void* stream) {
+  if (!k || !v || !k_cache || !v_cache || !block_table || !cache_lens) return S2ATTN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_rot == nullptr)) return S2ATTN_ERR_INVALID_ARG;
+  const void* ptrs[7] = {q, q_rot, k, k_rot, v, k_cache, v_cache};
+  for (const void* x : ptrs)
+    if (!aligned16(x)) return S2ATTN_ERR_INVALID_ARG;
+  if (T <= 0 || B <= 0 || (!cu_seqlens && T != B)) return S2ATTN_ERR_INVALID_ARG;
+  if (!(base > 1.f) || !std::isfinite(base) || !(pi_scale > 0.f) || !std::isfinite(pi_scale))
+    return S2ATTN_ERR_INVALID_ARG;
+  s2attn_status s = check_heads(Hq, Hkv, d);
+  if (s != S2ATTN_OK) return s;
+  s2::AppendParams p{};
+  if ((s = check_cache(Hkv, d, pages, page_size, max_pages, strides ? strides + 5 : nullptr, p.kc,
+                       p.vc)) != S2ATTN_OK)
+    return s;
+  const long long q_st = static_cast<long long>(Hq) * d, k_st = static_cast<long long>(Hkv) * d;
+  long long st[5] = {q_st, q_st, k_st, k_st, k_st};   // q, q_rot, k, k_rot, v
+  if (strides)
+    for (int i = 0; i < 5; ++i) {
+      st[i] = strides[i];
+      if (bad_row_stride(st[i], i < 2 ? Hq : Hkv, d)) return S2ATTN_ERR_INVALID_ARG;
+    }
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_rot = static_cast<__nv_bfloat16*>(q_rot);
+  p.k_rot = static_cast<__nv_bfloat16*>(k_rot);
+  p.q_st = st[0]; p.qr_st = st[1]; p.k_st = st[2]; p.kr_st = st[3]; p.v_st = st[4];
+  p.kc.p = static_cast<__nv_bfloat16*>(k_cache);
+  p.vc.p = static_cast<__nv_bfloat16*>(v_cache);
+  p.table = block_table; p.cu = cu_seqlens; p.lens = cache_lens;
+  p.T = T; p.B = B; p.Hq = q ? Hq : 0; p.Hkv = Hkv;
+  p.pages = pages; p.page_size = page_size; p.max_pages = max_pages;
+  const unsigned long long* f = turns(base, pi_scale, d);
+  std::copy(f, f + d / 2, p.turn);
+  int num_sms = 0;
+  if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
+  // Few token groups: the heads are split over the second axis until two blocks per SM exist.
+  const int groups = (T - 1) / s2::kAppendTokens + 1;
+  const int items = (p.Hq + 2 * Hkv) * (d / 16);
+  const int most = (items + s2::kAppendThreads - 1) / s2::kAppendThreads;
+  const int split = std::max(1, std::min(most, 2 * num_sms / groups));
+  const dim3 grid(groups, split);
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    s2::s2_append_kernel<64><<<grid, s2::kAppendThreads, 0, sm>>>(p);
+  else
+    s2::s2_append_kernel<128><<<grid, s2::kAppendThreads, 0, sm>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_append_kernel launch");
+}
+
+size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
+  if (B <= 0 || check_heads(Hq, Hkv, d) != S2ATTN_OK) return 0;
+  const DecodeSpace w = decode_space(B, Hq / Hkv, d);
+  return w.o + w.ml + w.plan;
+}
+
+s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                            const int* block_table, const int* cache_lens, void* o, float* lse,
+                            int B, int Hq, int Hkv, int d, int pages, int page_size, int max_pages,
+                            float scale, const long long* strides, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !block_table || !cache_lens || !o || !workspace)
+    return S2ATTN_ERR_INVALID_ARG;
+  const void* ptrs[4] = {q, k_cache, v_cache, o};
+  for (const void* x : ptrs)
+    if (!aligned16(x)) return S2ATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return S2ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || !(scale > 0.f) || !std::isfinite(scale)) return S2ATTN_ERR_INVALID_ARG;
+  s2attn_status s = check_heads(Hq, Hkv, d);
+  if (s != S2ATTN_OK) return s;
+  if (static_cast<long long>(B) * Hq >= (1ll << 31)) return S2ATTN_ERR_UNSUPPORTED;
+  s2::DecodeParams p{};
+  if ((s = check_cache(Hkv, d, pages, page_size, max_pages, strides ? strides + 2 : nullptr, p.kc,
+                       p.vc)) != S2ATTN_OK)
+    return s;
+  p.q_sb = p.o_sb = static_cast<long long>(Hq) * d;
+  if (strides) {
+    p.q_sb = strides[0];
+    p.o_sb = strides[1];
+    if (bad_row_stride(p.q_sb, Hq, d) || bad_row_stride(p.o_sb, Hq, d)) return S2ATTN_ERR_INVALID_ARG;
+  }
+  if (workspace_bytes < s2attn_decode_workspace_size(B, Hq, Hkv, d)) return S2ATTN_ERR_INVALID_ARG;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.kc.p = static_cast<__nv_bfloat16*>(const_cast<void*>(k_cache));
+  p.vc.p = static_cast<__nv_bfloat16*>(const_cast<void*>(v_cache));
+  p.table = block_table; p.lens = cache_lens;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv;
+  p.pages = pages; p.page_size = page_size; p.max_pages = max_pages;
+  p.group = Hq / Hkv;
+  p.chunks = (p.group + s2::kDecodeRows - 1) / s2::kDecodeRows;
+  p.rows = std::min(p.group, s2::kDecodeRows);
+  p.by_page = fast_div_by(page_size);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const DecodeSpace w = decode_space(B, p.group, d);
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.o);
+  p.plan = reinterpret_cast<long long*>(ws + w.o + w.ml);
+  int num_sms = 0;
+  if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
+  // No more CTAs than the longest batch the block table can describe has work for.
+  const long long tiles = static_cast<long long>(B) * Hkv * p.chunks *
+                          ((static_cast<long long>(max_pages) * page_size - 1) / s2::kDecodeTile + 1);
+  const int grid = static_cast<int>(std::min<long long>(std::min(num_sms, s2::kDecodeMaxCtas), tiles));
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_decode<64>(p, grid, sm) : launch_decode<128>(p, grid, sm);
+}
+
+}  // extern "C"

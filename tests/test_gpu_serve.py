@@ -1,0 +1,309 @@
+"""The serving operators on the GPU: rotation and append to a paged cache, and decode over it,
+against their definitions in 64 bits.
+
+Tolerances. A bf16 output is the kernel's fp32 value rounded once, off by at most half a step,
+2^-8 relative; the fp32 value itself differs from the exact one by
+* append: the sine's and cosine's fp32 errors (angle to 2^-25 turns = 2e-7 rad, sincospif to a few
+  2^-24) times |x|, so below 1e-6 (|x| + |y|);
+* attention: P rounded to bf16 for the product (2^-8 relative each, at most 2^-8 sum p |v| / sum p
+  <= 2^-8 max |v|), everything else in fp32 (below 1e-5 of the same). The bound used is
+  2^-8 |o| + (2^-8 + 1e-5) * (sum p |v| / sum p), element by element.
+LSE: fp32, scores of magnitude up to 2^5 or so: products summed in fp32 (128 terms, 2^-24 relative
+to sum |q k| <= 40 |s|-ish terms) and log2/exp2 approximations of 2^-22: 2e-5 absolute covers them.
+"""
+import random
+
+import pytest
+import torch
+
+import shifted_sparse_attention_fwd_b200 as s2
+
+pytestmark = pytest.mark.gpu
+
+BF16_STEP = 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s2.lib()
+
+
+def _ok():
+    torch.cuda.synchronize()
+    st, code = s2.s2attn_get_device_error()
+    assert st == s2.S2ATTN_OK, (st, hex(code))
+
+
+def _randn(seed, *shape):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _table(lens, page, seed, spare=2):
+    """Random pages for sequences of `lens` tokens; unused entries hold a number far outside."""
+    need = [-(-n // page) for n in lens]
+    order = list(range(sum(need) + spare))
+    random.Random(seed).shuffle(order)
+    width, rows, at = max(1, max(need)), [], 0
+    for n in need:
+        rows.append(order[at:at + n] + [1 << 30] * (width - n))
+        at += n
+    return rows, len(order)
+
+
+def _turn64(x, pos, base, pi):
+    d = x.shape[-1]
+    th = torch.tensor([base ** (-2.0 * i / d) for i in range(d // 2)], dtype=torch.float64, device=x.device)
+    a = (pos.double()[:, None] * pi * th)[:, None]
+    lo, hi = x[..., :d // 2].double(), x[..., d // 2:].double()
+    return torch.cat((lo * a.cos() - hi * a.sin(), hi * a.cos() + lo * a.sin()), -1)
+
+
+def _near_bf16(got, want, slack):
+    """|got - want| <= half a bf16 step of the value, plus `slack`."""
+    bad = (got.double() - want).abs() - (BF16_STEP * torch.maximum(got.double().abs(), want.abs()) + slack)
+    assert got.isfinite().all() and float(bad.max()) <= 0, float(bad.max())
+
+
+def _caches(seed, pages, page, hkv, d, layout):
+    if layout == "kv_by_page":       # [pages, 2, page, Hkv, d]
+        both = _randn(seed, pages, 2, page, hkv, d)
+        return both[:, 0], both[:, 1]
+    if layout == "kv_by_token":      # [pages, page, 2, Hkv, d]
+        both = _randn(seed, pages, page, 2, hkv, d)
+        return both[:, :, 0], both[:, :, 1]
+    return _randn(seed, pages, page, hkv, d), _randn(seed + 1, pages, page, hkv, d)
+
+
+# ------------------------------------------------------------------------------------------
+# rotation and append
+# ------------------------------------------------------------------------------------------
+APPEND = [
+    # new tokens, tokens before them, Hq, Hkv, d, page, pi_scale, layout
+    ([1], [0], 4, 4, 64, 1, 1.0, "apart"),
+    ([1, 1, 1], [0, 16, 4095], 8, 2, 128, 16, 0.5, "apart"),
+    ([5, 0, 1, 0, 0, 77], [0, 3, 100, 0, 9, 31], 6, 2, 128, 24, 0.25, "kv_by_page"),
+    ([9, 300, 8], [7, 1, 0], 5, 5, 64, 7, 1.0, "kv_by_token"),
+    ([3] * 40, list(range(40)), 2, 1, 64, 48, 1.0, "apart"),
+    ([2], [(1 << 24) - 40], 2, 2, 128, 1 << 16, 0.125, "apart"),      # a far position
+]
+
+
+@pytest.mark.parametrize("new,before,hq,hkv,d,page,pi,layout", APPEND)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_matches_formula(new, before, hq, hkv, d, page, pi, layout, in_place):
+    lens = [a + b for a, b in zip(new, before)]
+    if max(lens) >= 1 << 20:
+        # one huge virtual page table, all but the touched pages pointing at page 0
+        rows, pages = [[0] * (max(lens) // page) + [1]], 2
+        page_alloc = page
+    else:
+        rows, pages = _table(lens, page, 3)
+        page_alloc = page
+    T, behind = sum(new), 3
+    q, k, v = (_randn(11 + i, T + behind, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    kc, vc = _caches(20, pages, page_alloc, hkv, d, layout)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q_in, k_in, kc0, vc0 = q.clone(), k.clone(), kc.clone(), vc.clone()
+    q_rot = q if in_place else torch.full_like(q, 7.0)
+    k_rot = k if in_place else torch.full_like(k, 7.0)
+    s2.s2attn_rope_append(q, q_rot, k, k_rot, v, kc, vc, _ints(rows), _ints(lens), _ints(cu), pi_scale=pi)
+    _ok()
+    pos = torch.tensor([b + i for n, b in zip(new, before) for i in range(n)], device="cuda")
+    want_q, want_k = _turn64(q_in[:T], pos, 10000.0, pi), _turn64(k_in[:T], pos, 10000.0, pi)
+    slack = 1e-6 * 12                            # |x| + |y| below 12
+    _near_bf16(q_rot[:T], want_q, slack)
+    _near_bf16(k_rot[:T], want_k, slack)
+    # rows behind the last sequence stay as they were
+    assert torch.equal(q_rot[T:], q_in[T:] if in_place else torch.full_like(q_in[T:], 7.0))
+    assert torch.equal(k_rot[T:], k_in[T:] if in_place else torch.full_like(k_in[T:], 7.0))
+    # the cache: exactly these slots, with exactly these rows
+    seq = torch.tensor([s for s, n in enumerate(new) for _ in range(n)], device="cuda")
+    pg = torch.tensor(rows, device="cuda")[seq, pos // page]
+    kc0[pg, pos % page] = k_rot[:T]
+    vc0[pg, pos % page] = v[:T]
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+
+
+def test_append_token_form_idle_rows_and_no_queries():
+    lens, page, hkv, d = [5, 0, 33, 1], 8, 2, 64
+    rows, pages = _table(lens, page, 1)
+    k, v = _randn(1, 4, hkv, d), _randn(2, 4, hkv, d)
+    kc, vc = _randn(3, pages, page, hkv, d), _randn(4, pages, page, hkv, d)
+    kc0, vc0 = kc.clone(), vc.clone()
+    s2.s2attn_rope_append(None, None, k, None, v, kc, vc, _ints(rows), _ints(lens))
+    _ok()
+    for s in (0, 2, 3):
+        p = lens[s] - 1
+        want = _turn64(k[s:s + 1], torch.tensor([p], device="cuda"), 10000.0, 1.0)[0]
+        _near_bf16(kc[rows[s][p // page], p % page], want, 1.2e-5)
+        kc0[rows[s][p // page], p % page] = kc[rows[s][p // page], p % page]
+        vc0[rows[s][p // page], p % page] = v[s]
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+
+
+def test_append_bad_page_and_length_are_reported_and_skipped():
+    page, hkv, d = 8, 2, 64
+    for table, lens, site in (([[0], [5]], [3, 3], 0x80), ([[0], [-1]], [3, 3], 0x80), ([[0], [1]], [3, 9], 0x81)):
+        k, v = _randn(1, 2, hkv, d), _randn(2, 2, hkv, d)
+        kc, vc = _randn(3, 2, page, hkv, d), _randn(4, 2, page, hkv, d)
+        kc0, vc0 = kc.clone(), vc.clone()
+        s2.s2attn_rope_append(None, None, k, None, v, kc, vc, _ints(table), _ints(lens))
+        torch.cuda.synchronize()
+        assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (6 << 8) | site)
+        assert s2.s2attn_get_device_error() == (s2.S2ATTN_OK, 0)
+        kc0[0, 2], vc0[0, 2] = kc[0, 2], v[0]    # the good row's slot
+        assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+
+
+# ------------------------------------------------------------------------------------------
+# decode
+# ------------------------------------------------------------------------------------------
+def _decode64(q, kc, vc, rows, lens, scale):
+    B, hq, d = q.shape
+    page, hkv = kc.shape[1:3]
+    g = hq // hkv
+    o = torch.zeros(B, hq, d, dtype=torch.float64, device="cuda")
+    mean_abs = torch.zeros_like(o)
+    lse = torch.full((B, hq), float("-inf"), dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        t = torch.arange(n, device="cuda")
+        pg = torch.tensor(rows[b], device="cuda")[t // page]
+        k, v = kc[pg, t % page].double(), vc[pg, t % page].double()
+        for h in range(hq):
+            s = (k[:, h // g] @ q[b, h].double()) * scale
+            lse[b, h] = torch.logsumexp(s, 0)
+            p = torch.exp(s - lse[b, h])
+            o[b, h] = p @ v[:, h // g]
+            mean_abs[b, h] = p @ v[:, h // g].abs()
+    return o, lse, mean_abs
+
+
+def _check_decode(q, kc, vc, rows, lens, scale, o, lse):
+    want, want_lse, mean_abs = _decode64(q, kc, vc, rows, lens, scale)
+    _near_bf16(o, want, (BF16_STEP + 1e-5) * mean_abs)
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert (lse[empty] == float("-inf")).all() and (o[empty] == 0).all()
+    if not empty.all():
+        assert float((lse[~empty].double() - want_lse[~empty]).abs().max()) <= 2e-5
+
+
+DECODE = [
+    # lens, Hq, Hkv, d, page, layout
+    ([1], 1, 1, 64, 1, "apart"),
+    ([1, 2, 15, 16, 17, 31, 33], 4, 4, 128, 16, "apart"),
+    ([0, 130, 0, 0, 5], 8, 2, 64, 48, "kv_by_page"),
+    ([700, 1, 4097], 6, 2, 128, 24, "kv_by_token"),
+    ([513, 100], 16, 1, 128, 7, "apart"),          # a group of 16
+    ([300, 45], 17, 1, 64, 32, "apart"),           # a group over one MMA's rows, odd
+    ([90, 0, 1000], 40, 1, 128, 128, "apart"),     # three chunks of a group
+    ([9000], 64, 8, 128, 64, "apart"),             # one long sequence, split over every SM
+    ([33] * 300 + [0, 2000], 4, 4, 64, 16, "apart"),   # more sequences than a block has threads
+    ([0, 0], 4, 2, 64, 16, "apart"),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,page,layout", DECODE)
+def test_decode_matches_formula(lens, hq, hkv, d, page, layout):
+    rows, pages = _table(lens, page, 5)
+    kc, vc = _caches(30, pages, page, hkv, d, layout)
+    q = _randn(33, len(lens), hq, d) * 2
+    # what lies in the cache's other rows is never used
+    used = torch.zeros(pages, page, dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        if n:
+            used[torch.tensor(rows[b], device="cuda")[t // page], t % page] = True
+    for i, x in enumerate((kc, vc)):
+        bad = torch.full((1,), float("nan") if i else float("inf"), device="cuda", dtype=x.dtype)
+        x[~used] = bad
+    o, lse = s2.decode(q, kc, vc, _ints(rows), _ints(lens))
+    _ok()
+    _check_decode(q, kc, vc, rows, lens, d ** -0.5, o, lse)
+    o2, lse2 = s2.decode(q, kc, vc, _ints(rows), _ints(lens))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_bad_pages_and_lengths():
+    """A page outside the cache counts as zeros, a length is cut to the table: reported, not followed."""
+    page, hq, hkv, d = 16, 4, 2, 64
+    q, kc, vc = _randn(1, 2, hq, d), _randn(2, 4, page, hkv, d), _randn(3, 4, page, hkv, d)
+    for table, lens, site in (([[0, 1], [2, 4]], [20, 20], 0x80), ([[0, 1], [2, -7]], [20, 20], 0x80),
+                              ([[0, 1], [2, 3]], [20, 33], 0x81), ([[0, 1], [2, 3]], [20, -1], 0x81)):
+        o, lse = s2.decode(q, kc, vc, _ints(table), _ints(lens))
+        torch.cuda.synchronize()
+        assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (7 << 8) | site)
+        good_o, good_lse = s2.decode(q[:1], kc, vc, _ints(table[:1]), _ints(lens[:1]))
+        _ok()
+        assert torch.equal(lse[0], good_lse[0]) or float((lse[0] - good_lse[0]).abs().max()) < 1e-5
+
+
+def test_decode_on_another_stream_and_in_a_graph():
+    """A captured step follows the lengths and the tables of each replay."""
+    page, hq, hkv, d, B = 16, 8, 2, 128, 3
+    lens_list = [[40, 0, 1], [0, 333, 18], [512, 511, 513]]
+    kc, vc = _randn(2, 99, page, hkv, d), _randn(3, 99, page, hkv, d)
+    q = _randn(1, B, hq, d)
+    lens = _ints([1] * B)
+    table = torch.zeros(B, 33, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(B, hq, device="cuda")
+    ws = torch.empty(s2.s2attn_decode_workspace_size(B, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s2.s2attn_decode(q, kc, vc, table, lens, o, lse, workspace=ws, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s2.s2attn_decode(q, kc, vc, table, lens, o, lse, workspace=ws)
+    for i, ll in enumerate(lens_list):
+        rows, _ = _table(ll, page, i, spare=0)
+        full = [r[:33] + [1 << 30] * (33 - len(r)) for r in rows]
+        lens.copy_(_ints(ll))
+        table.copy_(_ints(full))
+        graph.replay()
+        _ok()
+        _check_decode(q, kc, vc, full, ll, d ** -0.5, o, lse)
+
+
+def test_append_then_decode_as_a_model_answers():
+    """Prompts appended, then three tokens appended and attended one by one, against attention in
+    64 bits over the rotated rows."""
+    hq, hkv, d, page, pi = 8, 2, 128, 16, 0.25
+    prompts, steps = [37, 1, 200], 3
+    lens = [n + steps for n in prompts]
+    rows, pages = _table(lens, page, 9)
+    table = _ints(rows)
+    kc, vc = torch.zeros(pages, page, hkv, d, dtype=torch.bfloat16, device="cuda"), \
+        torch.zeros(pages, page, hkv, d, dtype=torch.bfloat16, device="cuda")
+    cu = [0, 37, 38, 238]
+    q, k, v = (_randn(50 + i, 238, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    _, k_rot = s2.rope_append(q, k, v, kc, vc, table, _ints(prompts), _ints(cu), pi_scale=pi)
+    keys = [[k_rot[cu[b]:cu[b + 1]]] for b in range(3)]
+    vals = [[v[cu[b]:cu[b + 1]]] for b in range(3)]
+    for step in range(steps):
+        now = [n + step + 1 for n in prompts]
+        q, k, v = (_randn(60 + 3 * step + i, 3, h, d) for i, h in enumerate((hq, hkv, hkv)))
+        q_rot, k_rot = s2.rope_append(q, k, v, kc, vc, table, _ints(now), pi_scale=pi)
+        o, lse = s2.decode(q_rot, kc, vc, table, _ints(now))
+        _ok()
+        _near_bf16(q_rot, _turn64(q, torch.tensor(now, device="cuda") - 1, 10000.0, pi), 1.2e-5)
+        for b in range(3):
+            keys[b].append(k_rot[b:b + 1])
+            vals[b].append(v[b:b + 1])
+            kk, vv = torch.cat(keys[b]).double(), torch.cat(vals[b]).double()
+            assert kk.shape[0] == now[b]
+            for h in range(hq):
+                s = (kk[:, h // 4] @ q_rot[b, h].double()) * d ** -0.5
+                p = torch.softmax(s, 0)
+                _near_bf16(o[b, h], p @ vv[:, h // 4], (BF16_STEP + 1e-5) * (p @ vv[:, h // 4].abs()))
+                assert abs(float(lse[b, h]) - float(torch.logsumexp(s, 0))) <= 2e-5
