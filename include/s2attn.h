@@ -398,7 +398,7 @@ S2ATTN_API s2attn_status s2attn_rope_append(const void* q, void* q_rot, const vo
                                             float base, float pi_scale, const long long* strides,
                                             void* stream);
 
-/* Device workspace of s2attn_decode (256-byte aligned; contents on entry do not matter): about 20
+/* Device workspace of s2attn_decode (256-byte aligned; contents on entry do not matter): about 12
  * MB at d = 128 and 16 or more query heads per kv head, proportional to the smaller of that
  * group and 16. 0 for arguments s2attn_decode would reject. */
 S2ATTN_API size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d);

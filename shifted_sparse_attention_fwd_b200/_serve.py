@@ -15,6 +15,8 @@ import torch
 from ._lib import S2ATTN_OK, S2AttnError, _stream, lib
 
 _BF16, _I32 = torch.bfloat16, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, by device index
+_get_device = torch._C._cuda_getDevice
 
 
 def _on(stream, device):
@@ -26,50 +28,57 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _run(name, device, stream, call):
-    """call(stream handle) with `device` current; raises on a failed status."""
-    if device.index == torch.cuda.current_device():
-        status = call(_stream(stream))
+def _run(name, index, stream, args):
+    """The C function on device `index`, which is made current, with the stream's handle last."""
+    if stream is None:
+        handle = _raw_stream(index)
     else:
-        with torch.cuda.device(device):
-            status = call(_stream(stream))
+        handle = _stream(stream)
+    if index == _get_device():
+        status = getattr(lib(), name)(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), name)(*args, handle)
     if status != S2ATTN_OK:
         raise S2AttnError(status, name)
 
 
-def _rows(t, name, shape, device):
-    """Row stride of a bf16 [rows, heads, d] tensor whose (heads, d) block is contiguous."""
-    if t.dtype != _BF16:
-        raise ValueError(f"{name}: expected bf16, got {t.dtype}")
+def _check(name, t, dtype, shape, index):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    st = t.stride()
-    if st[2] != 1 or st[1] != shape[2]:
-        raise ValueError(f"{name}: expected contiguous (heads, d) blocks")
-    return st[0]
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name}: expected a CUDA tensor on device {index}, got {t.device}")
 
 
-def _cache_strides(t, name, shape, device):
-    """(page, token) strides of a bf16 [pages, page_size, Hkv, d] cache."""
-    if t.dtype != _BF16:
-        raise ValueError(f"{name}: expected bf16, got {t.dtype}")
-    if t.dim() != 4 or t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    st = t.stride()
-    if st[3] != 1 or st[2] != shape[3]:
-        raise ValueError(f"{name}: expected contiguous (Hkv, d) blocks")
-    return st[0], st[1]
+def _tensors(index, *named):
+    """Checks the (name, bf16 tensor or None, shape) of a call; whether all are contiguous."""
+    packed = True
+    for name, t, shape in named:
+        if t is None:
+            continue
+        # one cheap test for the usual case; _check says what is wrong
+        if t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or index < 0:
+            _check(name, t, _BF16, shape, index)
+        packed = packed and t.is_contiguous()
+    return packed
 
 
-def _ints(t, name, shape, device):
-    if t.dtype != _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _ints(index, name, t, shape):
+    if t.dtype is not _I32 or t.shape != shape or t.get_device() != index:
+        _check(name, t, _I32, shape, index)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
+
+
+def _outer_strides(name, t):
+    """Strides of the axes before a tensor's contiguous (heads, d) block."""
+    st = t.stride()
+    if st[-1] != 1 or st[-2] != t.shape[-1]:
+        raise ValueError(f"{name}: expected contiguous (heads, d) blocks")
+    return st[:-2]
 
 
 def s2attn_rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cache_lens,
@@ -78,32 +87,31 @@ def s2attn_rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cac
     into the paged cache (and k_rot unless None; may be k), and copy v [T,Hkv,d] into the cache.
     k_cache, v_cache [pages,page_size,Hkv,d]; block_table int32 [B,max_pages]; cache_lens int32 [B],
     the tokens of each sequence including the new ones; cu_seqlens int32 [B+1], the sequences' first
-    rows, or None for one new token per sequence. All but the strides is checked in include/s2attn.h's
-    terms; a bad page or length on the device is reported by s2attn_get_device_error."""
-    dev = k.device
-    T, Hkv, d = k.shape
+    rows, or None for one new token per sequence. Views with contiguous (heads, d) blocks are
+    accepted. A bad page or length on the device is reported by s2attn_get_device_error."""
+    index = k.get_device()
+    T, Hkv, d = rows = k.shape
     pages, page_size = k_cache.shape[:2]
     B, max_pages = block_table.shape
-    Hq, q_st, qr_st = Hkv, Hkv * d, Hkv * d
     if (q is None) != (q_rot is None):
         raise ValueError("q and q_rot go together")
-    if q is not None:
-        Hq = q.shape[1]
-        q_st, qr_st = _rows(q, "q", (T, Hq, d), dev), _rows(q_rot, "q_rot", (T, Hq, d), dev)
-    k_st, v_st = _rows(k, "k", k.shape, dev), _rows(v, "v", k.shape, dev)
-    kr_st = k_st if k_rot is None else _rows(k_rot, "k_rot", k.shape, dev)
-    cache = (pages, page_size, Hkv, d)
-    strides = (ctypes.c_longlong * 9)(
-        q_st, qr_st, k_st, kr_st, v_st, *_cache_strides(k_cache, "k_cache", cache, dev),
-        *_cache_strides(v_cache, "v_cache", cache, dev))
-    table = _ints(block_table, "block_table", (B, max_pages), dev)
-    lens = _ints(cache_lens, "cache_lens", (B,), dev)
-    cu = None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", (B + 1,), dev)
-    _run("s2attn_rope_append", dev, stream, lambda sm: lib().s2attn_rope_append(
+    Hq = Hkv if q is None else q.shape[1]
+    q_shape, cache = (T, Hq, d), (pages, page_size, Hkv, d)
+    named = (("q", q, q_shape), ("q_rot", q_rot, q_shape), ("k", k, rows), ("k_rot", k_rot, rows),
+             ("v", v, rows), ("k_cache", k_cache, cache), ("v_cache", v_cache, cache))
+    strides = None
+    if not _tensors(index, *named):
+        flat = []
+        for (name, t, _), like in zip(named, (None, q, None, k, None, None, None)):
+            flat += _outer_strides(name, t if t is not None else like if like is not None else k)
+        strides = (ctypes.c_longlong * 9)(*flat)
+    _run("s2attn_rope_append", index, stream, (
         None if q is None else q.data_ptr(), None if q is None else q_rot.data_ptr(), k.data_ptr(),
         None if k_rot is None else k_rot.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), table, cu, lens, T, B, Hq, Hkv, d, pages, page_size, max_pages, base,
-        pi_scale, strides, sm))
+        v_cache.data_ptr(), _ints(index, "block_table", block_table, (B, max_pages)),
+        None if cu_seqlens is None else _ints(index, "cu_seqlens", cu_seqlens, (B + 1,)),
+        _ints(index, "cache_lens", cache_lens, (B,)), T, B, Hq, Hkv, d, pages, page_size, max_pages,
+        base, pi_scale, strides))
 
 
 def s2attn_decode_workspace_size(B, Hq, Hkv, d) -> int:
@@ -116,29 +124,39 @@ def s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale=No
     None; caches, block_table and cache_lens as in s2attn_rope_append. workspace: a uint8 CUDA tensor
     of s2attn_decode_workspace_size bytes that no other running call uses, or None to let torch
     allocate it."""
-    dev = q.device
-    B, Hq, d = q.shape
+    index = q.get_device()
+    B, Hq, d = rows = q.shape
     pages, page_size, Hkv = k_cache.shape[:3]
     max_pages = block_table.shape[1]
     cache = (pages, page_size, Hkv, d)
-    strides = (ctypes.c_longlong * 6)(
-        _rows(q, "q", (B, Hq, d), dev), _rows(o, "o", (B, Hq, d), dev),
-        *_cache_strides(k_cache, "k_cache", cache, dev), *_cache_strides(v_cache, "v_cache", cache, dev))
-    table = _ints(block_table, "block_table", (B, max_pages), dev)
-    lens = _ints(cache_lens, "cache_lens", (B,), dev)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or lse.device != dev
-                            or not lse.is_contiguous()):
-        raise ValueError(f"lse: expected a contiguous fp32 tensor of shape {(B, Hq)} on {dev}")
+    named = (("q", q, rows), ("o", o, rows), ("k_cache", k_cache, cache), ("v_cache", v_cache, cache))
+    strides = None
+    if not _tensors(index, *named):
+        flat = []
+        for name, t, _ in named:
+            flat += _outer_strides(name, t)
+        strides = (ctypes.c_longlong * 6)(*flat)
+    if lse is not None:
+        _check("lse", lse, torch.float32, (B, Hq), index)
+        if not lse.is_contiguous():
+            raise ValueError("lse: expected a contiguous tensor")
     if workspace is None:
         n = s2attn_decode_workspace_size(B, Hq, Hkv, d)
-        with _on(stream, dev):
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
-    _run("s2attn_decode", dev, stream, lambda sm: lib().s2attn_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, lens, o.data_ptr(),
+        if stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:
+            with _on(stream, q.device):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        _check("workspace", workspace, torch.uint8, workspace.shape, index)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
+    _run("s2attn_decode", index, stream, (
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ints(index, "block_table", block_table, (B, max_pages)),
+        _ints(index, "cache_lens", cache_lens, (B,)), o.data_ptr(),
         None if lse is None else lse.data_ptr(), B, Hq, Hkv, d, pages, page_size, max_pages,
-        d ** -0.5 if scale is None else scale, strides, workspace.data_ptr(), workspace.numel(), sm))
+        d ** -0.5 if scale is None else scale, strides, workspace.data_ptr(), workspace.numel()))
 
 
 # ------------------------------------------------------------------------------------------

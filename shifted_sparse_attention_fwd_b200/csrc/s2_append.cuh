@@ -9,20 +9,21 @@
 // the host, rounded once), and t * F_i modulo 2^64 is the exact fraction of a turn (error
 // t * 2^-64). Its upper 32 bits, as a signed number, are sincospif's argument.
 //
-// Memory bound: every element is read once and written once or twice. A block takes 8 tokens, one
-// warp per token: the warp finds the token's sequence (32-way search of cu_seqlens), its slot, and
-// its D/2 angles, shared by all heads through shared memory. A thread then owns one 16-byte chunk
-// of a head's first half and its partner D/2 columns on, for all 8 tokens: 16 loads of 16 bytes in
-// flight a thread, the first ones issued before the slots and angles are known. A grid of few
-// blocks splits the heads over its second axis.
+// Memory bound: every element is read once and written once or twice. A block takes kTok tokens;
+// one lane per token finds its sequence (binary search of cu_seqlens) and slot, and all threads the
+// tokens' angles, shared by all heads through shared memory. The work then is units of one 16-byte
+// chunk of a head's first half and its partner D/2 columns on, for 8 tokens: 16 loads of 16 bytes in
+// flight a thread, the first ones issued before the slots and angles are known. 8 tokens a block
+// where the heads give a block's threads work, 32 where they do not (fewer than half a block's
+// threads). A grid of few blocks splits the heads over its second axis.
 #pragma once
 
 #include "s2_serve_common.cuh"
 
 namespace s2 {
 
-constexpr int kAppendTokens = 8;
-constexpr int kAppendThreads = 32 * kAppendTokens;
+constexpr int kAppendUnit = 8;            // tokens of a work unit
+constexpr int kAppendThreads = 256;
 
 struct AppendParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -35,36 +36,33 @@ struct AppendParams {
   unsigned long long turn[64];           // F_i
 };
 
-// The sequence that holds token t: the number of i in [1, B] with cu[i] <= t, by a whole warp.
+// The number of i in [1, B] with cu[i] <= t: the sequence that holds token t, B behind the last.
 __device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;                     // the answer lies in [lo, lo + n]
-  while (n > 0) {
-    const int step = (n + 31) / 32;
-    const int i = lo + (lane + 1) * step;
-    const bool below = i <= lo + n && cu[i] <= t;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, below));
-    lo += cnt * step;
-    n = step == 1 ? 0 : min(step - 1, B - lo);
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
   }
   return lo;
 }
 
-template <int D>
+template <int D, int kTok>
 __global__ void __launch_bounds__(kAppendThreads) s2_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kHalf = D / 2;
   constexpr int kChunks = D / 16;        // work items of a head: a 16-byte chunk and its partner
-  __shared__ float s_cos[kAppendTokens][kHalf], s_sin[kAppendTokens][kHalf];
-  __shared__ long long s_slot_k[kAppendTokens], s_slot_v[kAppendTokens];   // -1: not to be cached
-  __shared__ int s_live[kAppendTokens];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int t0 = blockIdx.x * kAppendTokens;
-  const int items = (p.Hq + 2 * p.Hkv) * kChunks;
+  constexpr int kSubs = kTok / kAppendUnit;
+  __shared__ float s_cos[kTok][kHalf], s_sin[kTok][kHalf];
+  __shared__ long long s_slot_k[kTok], s_slot_v[kTok];   // -1: not to be cached
+  __shared__ int s_pos[kTok];                            // -1: to be skipped
+  const int t_block = blockIdx.x * kTok;
+  const int items = (p.Hq + 2 * p.Hkv) * kChunks, units = items * kSubs;
   const int step = gridDim.y * kAppendThreads;
   int w = blockIdx.y * kAppendThreads + threadIdx.x;
 
-  uint4 lo[kAppendTokens], hi[kAppendTokens];
-  auto load = [&](int item) {
+  uint4 lo[kAppendUnit], hi[kAppendUnit];
+  auto load = [&](int unit) {
+    const int item = kSubs == 1 ? unit : unit % items;
+    const int t0 = t_block + (kSubs == 1 ? 0 : unit / items * kAppendUnit);
     const int h = item / kChunks, c = item % kChunks;
     const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
     const __nv_bfloat16* src = is_q ? p.q : is_k ? p.k : p.v;
@@ -72,75 +70,74 @@ __global__ void __launch_bounds__(kAppendThreads) s2_append_kernel(const __grid_
     const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
     src += t0 * st + static_cast<long long>(hh) * D + 8 * c;
 #pragma unroll
-    for (int tt = 0; tt < kAppendTokens; ++tt)
+    for (int tt = 0; tt < kAppendUnit; ++tt)
       if (t0 + tt < p.T) {
         lo[tt] = *reinterpret_cast<const uint4*>(src + tt * st);
         hi[tt] = *reinterpret_cast<const uint4*>(src + tt * st + kHalf);
       }
   };
-  if (w < items) load(w);
+  if (w < units) load(w);
 
-  // ---- this warp's token: position, slot, angles ----
-  {
-    const int t = t0 + warp;
+  // ---- the tokens' positions and slots, one lane each ----
+  if (threadIdx.x < kTok) {
+    const int t = t_block + threadIdx.x;
     long long pos = -1;
-    int seq = p.B;
+    int seq = t;
     if (t < p.T) {
       if (p.cu) {
         seq = find_sequence(p.cu, p.B, t);
         if (seq < p.B && t >= p.cu[seq])
           pos = static_cast<long long>(p.lens[seq]) - p.cu[seq + 1] + t;
       } else {
-        seq = t;
         pos = static_cast<long long>(p.lens[seq]) - 1;
       }
     }
-    if (lane == 0) {
-      long long sk = -1, sv = -1;
-      if (pos >= 0) {
-        if (pos >= static_cast<long long>(p.max_pages) * p.page_size) {
-          report_bad_index(p.err, KID_APPEND, kSiteBadLength);
-        } else {
-          const int slot_page = static_cast<int>(pos / p.page_size), at = static_cast<int>(pos % p.page_size);
-          const int page = p.table[static_cast<long long>(seq) * p.max_pages + slot_page];
-          if (page < 0 || page >= p.pages) {
-            report_bad_index(p.err, KID_APPEND, kSiteBadPage);
-          } else {
-            sk = page * p.kc.sp + at * p.kc.st;
-            sv = page * p.vc.sp + at * p.vc.st;
-          }
-        }
+    long long sk = -1, sv = -1;
+    if (pos >= static_cast<long long>(p.max_pages) * p.page_size) {
+      report_bad_index(p.err, KID_APPEND, kSiteBadLength);
+    } else if (pos >= 0) {
+      const int i = static_cast<int>(pos) / p.page_size, at = static_cast<int>(pos) % p.page_size;
+      const int page = p.table[static_cast<long long>(seq) * p.max_pages + i];
+      if (page < 0 || page >= p.pages) {
+        report_bad_index(p.err, KID_APPEND, kSiteBadPage);
+      } else {
+        sk = page * p.kc.sp + at * p.kc.st;
+        sv = page * p.vc.sp + at * p.vc.st;
       }
-      s_slot_k[warp] = sk;
-      s_slot_v[warp] = sv;
-      s_live[warp] = pos >= 0;
     }
-    if (pos >= 0) {
+    s_slot_k[threadIdx.x] = sk;
+    s_slot_v[threadIdx.x] = sv;
+    // (a position past 2^31 is reported above; it turns by the angle of the largest one)
+    s_pos[threadIdx.x] = pos < 0 ? -1 : pos > 0x7fffffff ? 0x7fffffff : static_cast<int>(pos);
+  }
+  __syncthreads();
 #pragma unroll
-      for (int i = lane; i < kHalf; i += 32) {
-        const unsigned long long turns = static_cast<unsigned long long>(pos) * p.turn[i];
-        float sv, cv;
-        sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f, &sv, &cv);
-        s_cos[warp][i] = cv;
-        s_sin[warp][i] = sv;
-      }
-    }
+  for (int k = threadIdx.x; k < kTok * kHalf; k += kAppendThreads) {
+    const int tt = k / kHalf, i = k % kHalf, pos = s_pos[tt];
+    if (pos < 0) continue;
+    const unsigned long long turns = static_cast<unsigned long long>(pos) * p.turn[i];
+    float sv, cv;
+    sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f, &sv, &cv);
+    s_cos[tt][i] = cv;
+    s_sin[tt][i] = sv;
   }
   __syncthreads();
 
-  for (; w < items; w += step) {
+  for (; w < units; w += step) {
     if (w >= step) load(w);
-    const int h = w / kChunks, c = w % kChunks;
+    const int item = kSubs == 1 ? w : w % items, sub = kSubs == 1 ? 0 : w / items * kAppendUnit;
+    const int h = item / kChunks, c = item % kChunks;
     const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
     const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
     const long long col = static_cast<long long>(hh) * D + 8 * c;
 #pragma unroll
-    for (int tt = 0; tt < kAppendTokens; ++tt) {
-      if (t0 + tt >= p.T || !s_live[tt]) continue;
-      uint4 olo = lo[tt], ohi = hi[tt];
+    for (int i = 0; i < kAppendUnit; ++i) {
+      const int tt = sub + i;
+      if (s_pos[tt] < 0) continue;
+      uint4 olo = lo[i], ohi = hi[i];
       if (is_q || is_k) {
-        const __nv_bfloat162* l2 = reinterpret_cast<const __nv_bfloat162*>(&lo[tt]);
-        const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&hi[tt]);
+        const __nv_bfloat162* l2 = reinterpret_cast<const __nv_bfloat162*>(&lo[i]);
+        const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&hi[i]);
         __nv_bfloat162* ol = reinterpret_cast<__nv_bfloat162*>(&olo);
         __nv_bfloat162* oh = reinterpret_cast<__nv_bfloat162*>(&ohi);
 #pragma unroll
@@ -158,9 +155,9 @@ __global__ void __launch_bounds__(kAppendThreads) s2_append_kernel(const __grid_
         *reinterpret_cast<uint4*>(dst + kHalf) = ohi;
       };
       if (is_q) {
-        store(p.q_rot + (t0 + tt) * p.qr_st + col);
+        store(p.q_rot + (t_block + tt) * p.qr_st + col);
       } else if (is_k) {
-        if (p.k_rot) store(p.k_rot + (t0 + tt) * p.kr_st + col);
+        if (p.k_rot) store(p.k_rot + (t_block + tt) * p.kr_st + col);
         if (s_slot_k[tt] >= 0) store(p.kc.p + s_slot_k[tt] + col);
       } else if (s_slot_v[tt] >= 0) {
         store(p.vc.p + s_slot_v[tt] + col);

@@ -6,13 +6,16 @@
 // K and V bound the kernel: two multiply-adds per element and query head.
 //
 // Split over the length: the batch is one list of 16-token tiles, sequence by sequence and inside
-// it head by head (a segment is one (sequence, head) pair's tiles). The list is cut into equal
-// contiguous ranges, one per warp of the grid, whatever the lengths are, so a ragged batch and a
+// it head by head (a segment is one (sequence, head) pair's tiles, with kDecodeGap empty places
+// before them for what a segment's start and end cost). The list is cut into equal contiguous
+// ranges, one per CTA and in it one per warp, whatever the lengths are, so a ragged batch and a
 // single long sequence load every SM alike. The lengths are read on the device: one launch, and a
-// captured graph, serves every length. A segment inside one range is finished by its warp; of the
-// others each warp leaves at most two partial results (running maximum, sum and unnormalised
-// output in fp32) in the workspace, which a second small kernel joins in the order of the ranges
-// (no atomics: the same bits every time). It is launched programmatically early and waits there.
+// captured graph, serves every length. A segment inside one warp's range is finished by that warp.
+// The pieces (running maximum, sum and unnormalised output in fp32) of the others are joined first
+// inside the CTA, through shared memory; of the segments that cross CTAs, at most two a CTA, the
+// partial results go to the workspace, and a second small kernel, one block per CTA boundary and
+// query row, joins them. Pieces are always added in the list's order, with no atomics: the same
+// bits every time. The second kernel is launched programmatically early and waits on the device.
 //
 // A warp is on its own: it copies its tiles' rows to its part of shared memory with 16-byte
 // asynchronous copies (the row's page looked up one tile ahead), kDecodeStages tiles deep, so
@@ -32,6 +35,7 @@ constexpr int kDecodeWarps = 8;
 constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kDecodeTile = 16;           // tokens
 constexpr int kDecodeRows = 16;           // query heads a warp takes at a time (one MMA's rows)
+constexpr int kDecodeGap = 1;
 constexpr int kDecodeMaxCtas = 148;       // the workspace has room for this many CTAs' partials
 constexpr int kDecodeJoinThreads = 256;
 
@@ -44,6 +48,13 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
   return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned int>(n)) * f.mul) >> f.shift);
 }
 
+// The segment that begins in a CTA's range and goes on behind it.
+struct DecodeTail {
+  long long begin;                        // list place of its first tile
+  long long cta_range;                    // places of a CTA's range
+  int b, hv, tiles, valid;
+};
+
 struct DecodeParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
@@ -55,9 +66,10 @@ struct DecodeParams {
   int group, chunks;                      // query heads per kv head, and their chunks of 16
   FastDiv by_page;
   float scale_log2;
-  float* part_o;                          // [warps][2][rows][D]
-  float2* part_ml;                        // [warps][2][rows]: running maximum (log2 units), sum
-  long long* plan;                        // [0]: tiles per warp; [1 + b]: first tile of sequence b / (Hkv chunks)
+  float* first_o;                         // [warps][rows][D]: pieces of a warp's first segment
+  float* part_o;                          // [CTAs][2][rows][D]: partials of segments across CTAs
+  float2* part_ml;                        // [CTAs][2][rows]: running maximum (log2 units), sum
+  struct DecodeTail* tail;                // [CTAs]
   int rows;                               // query rows of a partial: min(group, 16)
   unsigned int* err;
 };
@@ -99,23 +111,38 @@ __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
 }
 __device__ __forceinline__ int decode_tiles(int len) { return len / kDecodeTile + (len % kDecodeTile != 0); }
 
-// A place in the list of tiles.
+// A tile: its sequence, head, number in the segment, and its place in the list.
 struct DecodeAt {
   int b, hv, tile, tiles, len;            // hv = kv head * chunks + chunk of its query heads
+  long long place;
 };
 
-template <int D>
+// The query heads of a segment: the first one, and how many.
+__device__ __forceinline__ int decode_heads(const DecodeParams& p, int hv, int& h0) {
+  const int kvh = p.chunks == 1 ? hv : hv / p.chunks;
+  h0 = kvh * p.group + (hv - kvh * p.chunks) * kDecodeRows;
+  return min(kDecodeRows, (kvh + 1) * p.group - h0);
+}
+
+// ROWS: 8 or 16 query rows a warp computes (the MMA has 16; with 8 the upper ones' softmax is left out).
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __grid_constant__ DecodeParams p) {
   using L = DecodeLayout<D>;
-  constexpr int kSteps = D / 16;
+  constexpr int kSteps = D / 16, kHalves = ROWS / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_pre[kDecodeThreads + 1];
+  __shared__ long long s_pre[kDecodeThreads + 1], s_warp[kDecodeWarps];
+  // The pieces of segments that did not end where they began: of each warp's first segment and of
+  // its last. kind 0: none, 1: output in first_o, 2: in the warp's part of shared memory.
+  __shared__ struct { long long begin; int b, hv, tiles, kind; } s_piece[2 * kDecodeWarps];
+  __shared__ float2 s_ml[2 * kDecodeWarps][ROWS];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_launch_dependents();
+  if (threadIdx.x < 2 * kDecodeWarps) s_piece[threadIdx.x].kind = 0;
 
-  // ---- the plan: tiles before every run of `per` sequences ----
+  // ---- the list: places before every run of `per` sequences ----
   const int hv_count = p.Hkv * p.chunks;
   const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;
+  auto places = [](int tiles) { return tiles == 0 ? 0 : tiles + kDecodeGap; };   // of one segment
   {
     long long sum = 0;
     for (int i = 0; i < per; ++i) {
@@ -123,7 +150,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
       if (b >= p.B) break;
       const int n = p.lens[b], len = decode_len(p, b);
       if (blockIdx.x == 0 && n != len) report_bad_index(p.err, KID_DECODE, kSiteBadLength);
-      sum += decode_tiles(len);
+      sum += places(decode_tiles(len));
     }
     long long inc = sum;                  // inclusive scan: in the warp, then over the warps
 #pragma unroll
@@ -131,58 +158,53 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
       const long long up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
-    __shared__ long long s_warp[kDecodeWarps];
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
     for (int i = 0; i < warp; ++i) inc += s_warp[i];
     s_pre[threadIdx.x + 1] = inc;
     if (threadIdx.x == 0) s_pre[0] = 0;
     __syncthreads();
-    if (blockIdx.x == 0) {                // for the joining kernel
-      long long at = inc - sum;
-      for (int i = 0; i < per; ++i) {
-        const int b = threadIdx.x * per + i;
-        if (b >= p.B) break;
-        p.plan[1 + b] = at;
-        at += decode_tiles(decode_len(p, b));
-      }
-    }
   }
   const long long total = s_pre[kDecodeThreads] * hv_count;
-  const long long n_warps = static_cast<long long>(gridDim.x) * kDecodeWarps;
-  const long long range = (total + n_warps - 1) / n_warps;
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.plan[0] = range;
-  // neighbouring ranges on different SMs: a short list spreads over all of them
-  const long long gw = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-  const long long first = gw * range, last = first + range < total ? first + range : total;
-  if (first >= last) return;
+  const long long cta_range = (total + gridDim.x - 1) / gridDim.x;
+  const long long cta_first = blockIdx.x * cta_range;
+  const long long cta_last = cta_first + cta_range < total ? cta_first + cta_range : total;
+  const long long warp_range = (cta_range + kDecodeWarps - 1) / kDecodeWarps;
+  const long long first = cta_first + warp * warp_range;
+  const long long last = first + warp_range < cta_last ? first + warp_range : cta_last;
 
   // ---- where the range begins ----
-  DecodeAt at;
-  long long seg_begin;                    // the list index of the current segment's first tile
-  {
-    const long long x = first;
-    int lo = 0, hi = kDecodeThreads;      // the last run that begins at or before x
+  DecodeAt at{};
+  at.place = last;                        // nothing to do
+  if (first < last) {
+    int lo = 0, hi = kDecodeThreads;      // the last run that begins at or before the range
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (s_pre[mid] * hv_count <= x) lo = mid; else hi = mid;
+      if (s_pre[mid] * hv_count <= first) lo = mid; else hi = mid;
     }
     long long begin = s_pre[lo];
     at.b = lo * per;
     for (;;) {
       at.len = decode_len(p, at.b);
       at.tiles = decode_tiles(at.len);
-      if (x < (begin + at.tiles) * hv_count) break;
-      begin += at.tiles;
+      if (first < (begin + places(at.tiles)) * hv_count) break;
+      begin += places(at.tiles);
       ++at.b;
     }
-    const long long in = x - begin * hv_count;
-    at.hv = static_cast<int>(in / at.tiles);
-    at.tile = static_cast<int>(in % at.tiles);
-    seg_begin = x - at.tile;
+    const long long in = first - begin * hv_count;
+    at.hv = static_cast<int>(in / places(at.tiles));
+    at.tile = static_cast<int>(in % places(at.tiles)) - kDecodeGap;
+    at.place = first;
+    if (at.tile < 0) {                    // in the gap before a segment
+      at.place -= at.tile;
+      at.tile = 0;
+    }
   }
-  auto advance = [&](DecodeAt& a) {       // the next tile (only while one is left in the range)
+  auto advance = [&](DecodeAt& a) {       // the next tile, if its place is still in the range
+    ++a.place;
     if (++a.tile < a.tiles) return;
+    a.place += kDecodeGap;
+    if (a.place >= last) return;
     a.tile = 0;
     if (++a.hv < hv_count) return;
     a.hv = 0;
@@ -196,7 +218,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   // ---- copies ----
   constexpr int kChunks = D / 8;                     // 16-byte chunks of a row
   constexpr int kRowsPer = 32 / kChunks;             // rows a warp copies with one instruction
-  const uint32_t ring = smem_u32(smem) + warp * (L::kStages * L::kStage);
+  uint8_t* const ring_p = smem + warp * (L::kStages * L::kStage);
+  const uint32_t ring = smem_u32(ring_p);
   int page, slot;                                    // of row lane % 16 of the load cursor's tile
   auto look_up = [&](const DecodeAt& a) {
     const int t = a.tile * kDecodeTile + (lane & 15);
@@ -213,12 +236,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     }
   };
   DecodeAt ld = at;
-  const int n_tiles = static_cast<int>(last - first);
-  int loaded = 0;
-  look_up(ld);
+  int load_stage = 0;
+  if (ld.place < last) look_up(ld);
   auto issue = [&]() {                               // the next tile's rows into its stage
-    if (loaded < n_tiles) {
-      const uint32_t dst = ring + (loaded % L::kStages) * L::kStage;
+    if (ld.place < last) {
+      const uint32_t dst = ring + load_stage * L::kStage;
+      load_stage = load_stage + 1 == L::kStages ? 0 : load_stage + 1;
       const int kvh = p.chunks == 1 ? ld.hv : ld.hv / p.chunks;
       const int c = lane % kChunks;
       const long long col = static_cast<long long>(kvh) * D + 8 * c;
@@ -232,45 +255,60 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
         decode_copy16(dst + off, p.kc.p + pz * p.kc.sp + sl * p.kc.st + col, on);
         decode_copy16(dst + L::kHalf + off, p.vc.p + pz * p.vc.sp + sl * p.vc.st + col, on);
       }
-      if (++loaded < n_tiles) {
-        advance(ld);
-        look_up(ld);
-      }
+      advance(ld);
+      if (ld.place < last) look_up(ld);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int s = 0; s < L::kStages - 1; ++s) issue();
 
+  // Rows of empty sequences, while the first copies are on their way.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (decode_len(p, b) != 0) continue;
+    for (int i = threadIdx.x; i < p.Hq * D; i += kDecodeThreads) p.o[b * p.o_sb + i] = __float2bfloat16(0.f);
+    if (p.lse)
+      for (int i = threadIdx.x; i < p.Hq; i += kDecodeThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
+  }
+
   // ---- the range, tile by tile ----
   const int r0 = lane / 4, c0 = 2 * (lane % 4);
   uint32_t qf[kSteps][4];
   float acc[D / 8][4];
-  float m[2], l[2];
-  for (int n = 0; n < n_tiles; ++n) {
-    const int kvh = p.chunks == 1 ? at.hv : at.hv / p.chunks;
-    const int h0 = kvh * p.group + (at.hv - kvh * p.chunks) * kDecodeRows;
-    const int rows = min(kDecodeRows, (kvh + 1) * p.group - h0);
-    if (n == 0 || at.tile == 0) {                    // a segment begins: its queries, empty state
+  float m[kHalves], l[kHalves];
+  int stage = 0;
+  bool fresh = true;                                 // a segment begins here, for this warp
+  int seg_tile = 0;                                  // ... at this tile of it
+  while (at.place < last) {
+    int h0;
+    const int rows = decode_heads(p, at.hv, h0);
+    if (fresh) {                                     // its queries, empty state
       const __nv_bfloat16* qb = p.q + at.b * p.q_sb + static_cast<long long>(h0) * D + c0;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = r0 + 8 * (e & 1);
-          qf[k][e] = row < rows ? *reinterpret_cast<const uint32_t*>(qb + row * D + 16 * k + 8 * (e >> 1)) : 0u;
+          qf[k][e] = row < ROWS && row < rows
+                         ? *reinterpret_cast<const uint32_t*>(qb + row * D + 16 * k + 8 * (e >> 1)) : 0u;
         }
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHalves; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      seg_tile = at.tile;
+      fresh = false;
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 2) : "memory");
     __syncwarp();                                    // every lane's copies, and the stage freed below
     issue();
-    const uint32_t ks = ring + (n % L::kStages) * L::kStage, vs = ks + L::kHalf;
+    const uint32_t ks = ring + stage * L::kStage, vs = ks + L::kHalf;
+    stage = stage + 1 == L::kStages ? 0 : stage + 1;
 
     float s[2][4] = {};
 #pragma unroll
@@ -289,9 +327,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
         for (int e = 0; e < 4; ++e)
           if (8 * t + c0 + (e & 1) >= left) s[t][e] = -INFINITY;
     }
-    uint32_t pf[4];
+    uint32_t pf[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {           // rows r0 and r0 + 8
+    for (int half = 0; half < kHalves; ++half) {     // rows r0 and r0 + 8
       float mx = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -325,72 +363,126 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
       mma_bf16(acc[2 * j + 1], pf, vb[2], vb[3]);
     }
 
-    const bool seg_end = at.tile + 1 == at.tiles;
-    if (seg_end || n + 1 == n_tiles) {
-      const bool whole = seg_end && seg_begin >= first;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-        const int row = r0 + 8 * half;
-        if (row >= rows) continue;
-        if (whole) {
-          const float inv = 1.f / l[half];
-          __nv_bfloat16* ob = p.o + at.b * p.o_sb + static_cast<long long>(h0 + row) * D + c0;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<uint32_t*>(ob + 8 * j) = pack_bf16(acc[j][2 * half] * inv, acc[j][2 * half + 1] * inv);
-          if (p.lse && lane % 4 == 0)
-            p.lse[static_cast<long long>(at.b) * p.Hq + h0 + row] =
-                (m[half] + log2f(l[half])) * 0.6931471805599453f;
-        } else {
-          // partial 0: the segment holds the range's first tile; 1: it begins inside the range
-          const long long part = (gw * 2 + (seg_begin > first ? 1 : 0)) * p.rows + row;
-          float* ob = p.part_o + part * D + c0;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<float2*>(ob + 8 * j) = make_float2(acc[j][2 * half], acc[j][2 * half + 1]);
-          if (lane % 4 == 0) p.part_ml[part] = make_float2(m[half], l[half]);
-        }
+    const DecodeAt now = at;
+    advance(at);
+    const bool seg_end = now.tile + 1 == now.tiles, end = at.place >= last;
+    if (!seg_end && !end) continue;
+    fresh = true;
+    const bool whole = seg_end && seg_tile == 0;
+    const int piece = 2 * warp + (end ? 1 : 0);
+    float* out = p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + warp) * p.rows * D;
+    if (!whole) {
+      if (end) {                                     // the ring is free: every tile has been used
+        __syncwarp();
+        out = reinterpret_cast<float*>(ring_p);
+      }
+      if (lane == 0) {
+        s_piece[piece].begin = now.place - now.tile;
+        s_piece[piece].b = now.b;
+        s_piece[piece].hv = now.hv;
+        s_piece[piece].tiles = now.tiles;
+        s_piece[piece].kind = end ? 2 : 1;
       }
     }
-    if (n + 1 < n_tiles) {
-      if (seg_end) seg_begin = first + n + 1;
-      advance(at);
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+      const int row = r0 + 8 * half;
+      if (row >= rows) continue;
+      if (whole) {
+        const float inv = 1.f / l[half];
+        __nv_bfloat16* ob = p.o + now.b * p.o_sb + static_cast<long long>(h0 + row) * D + c0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<uint32_t*>(ob + 8 * j) = pack_bf16(acc[j][2 * half] * inv, acc[j][2 * half + 1] * inv);
+        if (p.lse && lane % 4 == 0)
+          p.lse[static_cast<long long>(now.b) * p.Hq + h0 + row] = (m[half] + log2f(l[half])) * 0.6931471805599453f;
+      } else {
+        float* ob = out + row * D + c0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2*>(ob + 8 * j) = make_float2(acc[j][2 * half], acc[j][2 * half + 1]);
+        if (lane % 4 == 0) s_ml[piece][row] = make_float2(m[half], l[half]);
+      }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  // ---- join the CTA's pieces, segment by segment ----
+  if (threadIdx.x == 0) p.tail[blockIdx.x].valid = 0;
+  for (int i = 0; i < 2 * kDecodeWarps;) {
+    if (s_piece[i].kind == 0) {
+      ++i;
+      continue;
+    }
+    const long long begin = s_piece[i].begin;
+    const int b = s_piece[i].b, hv = s_piece[i].hv, tiles = s_piece[i].tiles;
+    int j = i + 1;
+    while (j < 2 * kDecodeWarps && (s_piece[j].kind == 0 || s_piece[j].begin == begin)) ++j;
+    int h0;
+    const int rows = decode_heads(p, hv, h0);
+    const bool starts = begin >= cta_first, ends = begin + tiles <= cta_last;
+    for (int u = threadIdx.x; u < rows * (D / 4); u += kDecodeThreads) {
+      const int row = u / (D / 4), col = 4 * (u % (D / 4));
+      float mt = -INFINITY, lt = 0.f;
+      for (int k = i; k < j; ++k)
+        if (s_piece[k].kind) mt = fmaxf(mt, s_ml[k][row].x);
+      const float mu = mt == -INFINITY ? 0.f : mt;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = i; k < j; ++k) {
+        const int kind = s_piece[k].kind;
+        if (kind == 0) continue;
+        const float* src = kind == 1
+            ? p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + k / 2) * p.rows * D
+            : reinterpret_cast<const float*>(smem + (k / 2) * (L::kStages * L::kStage));
+        const float4 x = *reinterpret_cast<const float4*>(src + row * D + col);
+        const float w = fast_exp2(s_ml[k][row].x - mu);
+        lt = fmaf(s_ml[k][row].y, w, lt);
+        sum.x = fmaf(x.x, w, sum.x);
+        sum.y = fmaf(x.y, w, sum.y);
+        sum.z = fmaf(x.z, w, sum.z);
+        sum.w = fmaf(x.w, w, sum.w);
+      }
+      if (starts && ends) {
+        const float inv = 1.f / lt;
+        uint2 w2;
+        w2.x = pack_bf16(sum.x * inv, sum.y * inv);
+        w2.y = pack_bf16(sum.z * inv, sum.w * inv);
+        *reinterpret_cast<uint2*>(p.o + b * p.o_sb + static_cast<long long>(h0 + row) * D + col) = w2;
+        if (p.lse && col == 0)
+          p.lse[static_cast<long long>(b) * p.Hq + h0 + row] = (mt + log2f(lt)) * 0.6931471805599453f;
+      } else {
+        const long long part = (blockIdx.x * 2ll + (starts ? 1 : 0)) * p.rows + row;
+        *reinterpret_cast<float4*>(p.part_o + part * D + col) = sum;
+        if (col == 0) p.part_ml[part] = make_float2(mt, lt);
+      }
+    }
+    if (starts && !ends && threadIdx.x == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
+    i = j;
+  }
 }
 
-// Joins the partials of the segments that more than one warp worked on, and writes the rows of
-// empty sequences (o = 0, lse = -inf). One block per (sequence, query head): each warp takes every
-// eighth partial's row (a float4 or float2 a lane), then the warps' sums are added in order.
+// Joins the partials of the segments that cross CTAs: block (c, row) that query row of the segment
+// that begins in CTA c's range and goes on behind it, if there is one. Each warp takes every eighth
+// partial's row (a float4 or float2 a lane), then the warps' sums are added in order.
 template <int D>
 __global__ void __launch_bounds__(kDecodeJoinThreads) s2_decode_join_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kWarps = kDecodeJoinThreads / 32;
   constexpr int kPer = D / 32;
   __shared__ float s_o[kWarps][D];
   __shared__ float2 s_ml[kWarps];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int kvh = h / p.group, in_group = h - kvh * p.group;
-  const int hv = kvh * p.chunks + in_group / kDecodeRows, row = in_group % kDecodeRows;
-  const int tiles = decode_tiles(decode_len(p, b));
+  const int cta = blockIdx.x, row = blockIdx.y;
   pdl_wait();
-  if (tiles == 0) {
-    for (int c = threadIdx.x; c < D; c += kDecodeJoinThreads)
-      p.o[b * p.o_sb + static_cast<long long>(h) * D + c] = __float2bfloat16(0.f);
-    if (p.lse && threadIdx.x == 0) p.lse[static_cast<long long>(b) * p.Hq + h] = -INFINITY;
-    return;
-  }
-  const long long range = p.plan[0];
-  const long long t0 = p.plan[1 + b] * (p.Hkv * p.chunks) + static_cast<long long>(hv) * tiles;
-  const long long w0 = t0 / range, w1 = (t0 + tiles - 1) / range;
-  if (w0 == w1) return;                   // one warp had it all and wrote the result
-  const int n = static_cast<int>(w1 - w0) + 1;
-  auto part = [&](int i) {
-    return ((w0 + i) * 2 + (i == 0 && t0 > w0 * range ? 1 : 0)) * p.rows + row;
-  };
+  const DecodeTail t = p.tail[cta];
+  if (!t.valid) return;
+  int h0;
+  if (row >= decode_heads(p, t.hv, h0)) return;
+  // partial 0: CTA `cta`, where the segment begins (its second slot); i: CTA `cta` + i's first slot
+  const int n = static_cast<int>((t.begin + t.tiles - 1) / t.cta_range) - cta + 1;
+  auto part = [&](int i) { return ((cta + i) * 2ll + (i == 0 ? 1 : 0)) * p.rows + row; };
   float m = -INFINITY, l = 0.f, acc[kPer] = {};
   for (int base = warp; base < n; base += 32 * kWarps) {
     const int i = base + kWarps * lane, cnt = min(32, (n - base + kWarps - 1) / kWarps);
@@ -436,9 +528,9 @@ __global__ void __launch_bounds__(kDecodeJoinThreads) s2_decode_join_kernel(cons
       lt = fmaf(s_ml[i].y, w, lt);
       ot = fmaf(s_o[i][threadIdx.x], w, ot);
     }
-    p.o[b * p.o_sb + static_cast<long long>(h) * D + threadIdx.x] = __float2bfloat16(ot / lt);
+    p.o[t.b * p.o_sb + static_cast<long long>(h0 + row) * D + threadIdx.x] = __float2bfloat16(ot / lt);
     if (p.lse && threadIdx.x == 0)
-      p.lse[static_cast<long long>(b) * p.Hq + h] = (mt + log2f(lt)) * 0.6931471805599453f;
+      p.lse[static_cast<long long>(t.b) * p.Hq + h0 + row] = (mt + log2f(lt)) * 0.6931471805599453f;
   }
 }
 

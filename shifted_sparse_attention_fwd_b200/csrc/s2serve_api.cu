@@ -33,7 +33,10 @@ ServeDevice g_serve_dev[kMaxDevices];
 
 template <int D>
 cudaError_t serve_smem_attrs() {
-  return cudaFuncSetAttribute(s2::s2_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(
+      s2::s2_decode_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2::DecodeLayout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(s2::s2_decode_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               s2::DecodeLayout<D>::kBytes);
 }
 
@@ -110,28 +113,48 @@ const unsigned long long* turns(float base, float pi_scale, int d) {
   return last.f;
 }
 
+// 32 tokens a block where one token's heads would leave more than half of a block idle and the
+// tokens still fill the GPU; the heads split over the second axis until two blocks per SM exist.
+template <int D>
+void launch_append(const s2::AppendParams& p, int num_sms, cudaStream_t stream) {
+  const int items = (p.Hq + 2 * p.Hkv) * (D / 16);
+  const bool wide = items <= s2::kAppendThreads / 2 && p.T >= 32 * num_sms;
+  const int tok = wide ? 32 : s2::kAppendUnit;
+  const int groups = (p.T - 1) / tok + 1;
+  const int most = (items * (tok / s2::kAppendUnit) + s2::kAppendThreads - 1) / s2::kAppendThreads;
+  const dim3 grid(groups, std::max(1, std::min(most, 2 * num_sms / groups)));
+  if (wide)
+    s2::s2_append_kernel<D, 32><<<grid, s2::kAppendThreads, 0, stream>>>(p);
+  else
+    s2::s2_append_kernel<D, s2::kAppendUnit><<<grid, s2::kAppendThreads, 0, stream>>>(p);
+}
+
 constexpr size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-// Workspace of the decode: partial outputs | partial {max, sum} | plan.
+// Workspace of the decode: first pieces | partial outputs | partial {max, sum} | tails.
 struct DecodeSpace {
-  size_t o, ml, plan;
+  size_t first, part, ml, tail;
 };
-DecodeSpace decode_space(int B, int group, int d) {
-  const size_t slots = static_cast<size_t>(s2::kDecodeMaxCtas) * s2::kDecodeWarps * 2 *
-                       std::min(group, s2::kDecodeRows);
-  return {round256(slots * d * sizeof(float)), round256(slots * sizeof(float2)),
-          round256((static_cast<size_t>(B) + 1) * sizeof(long long))};
+DecodeSpace decode_space(int group, int d) {
+  const size_t ctas = s2::kDecodeMaxCtas, rows = std::min(group, s2::kDecodeRows);
+  return {round256(ctas * s2::kDecodeWarps * rows * d * sizeof(float)),
+          round256(ctas * 2 * rows * d * sizeof(float)), round256(ctas * 2 * rows * sizeof(float2)),
+          round256(ctas * sizeof(s2::DecodeTail))};
 }
 
 template <int D>
 s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t stream) {
-  s2::s2_decode_kernel<D><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
+  if (p.rows <= 8)
+    s2::s2_decode_kernel<D, 8><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
+  else
+    s2::s2_decode_kernel<D, 16><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "s2_decode_kernel launch");
+  if (grid == 1) return S2ATTN_OK;   // nothing crosses CTAs
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq);
+  cfg.gridDim = dim3(grid - 1, p.rows);
   cfg.blockDim = dim3(s2::kDecodeJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -186,25 +209,19 @@ s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void
   std::copy(f, f + d / 2, p.turn);
   int num_sms = 0;
   if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
-  // Few token groups: the heads are split over the second axis until two blocks per SM exist.
-  const int groups = (T - 1) / s2::kAppendTokens + 1;
-  const int items = (p.Hq + 2 * Hkv) * (d / 16);
-  const int most = (items + s2::kAppendThreads - 1) / s2::kAppendThreads;
-  const int split = std::max(1, std::min(most, 2 * num_sms / groups));
-  const dim3 grid(groups, split);
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    s2::s2_append_kernel<64><<<grid, s2::kAppendThreads, 0, sm>>>(p);
+    launch_append<64>(p, num_sms, sm);
   else
-    s2::s2_append_kernel<128><<<grid, s2::kAppendThreads, 0, sm>>>(p);
+    launch_append<128>(p, num_sms, sm);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_append_kernel launch");
 }
 
 size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
   if (B <= 0 || check_heads(Hq, Hkv, d) != S2ATTN_OK) return 0;
-  const DecodeSpace w = decode_space(B, Hq / Hkv, d);
-  return w.o + w.ml + w.plan;
+  const DecodeSpace w = decode_space(Hq / Hkv, d);
+  return w.first + w.part + w.ml + w.tail;
 }
 
 s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_cache,
@@ -246,16 +263,18 @@ s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_ca
   p.rows = std::min(p.group, s2::kDecodeRows);
   p.by_page = fast_div_by(page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
-  const DecodeSpace w = decode_space(B, p.group, d);
+  const DecodeSpace w = decode_space(p.group, d);
   char* ws = static_cast<char*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + w.o);
-  p.plan = reinterpret_cast<long long*>(ws + w.o + w.ml);
+  p.first_o = reinterpret_cast<float*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + w.first);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.first + w.part);
+  p.tail = reinterpret_cast<s2::DecodeTail*>(ws + w.first + w.part + w.ml);
   int num_sms = 0;
   if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
   // No more CTAs than the longest batch the block table can describe has work for.
   const long long tiles = static_cast<long long>(B) * Hkv * p.chunks *
-                          ((static_cast<long long>(max_pages) * page_size - 1) / s2::kDecodeTile + 1);
+                          ((static_cast<long long>(max_pages) * page_size - 1) / s2::kDecodeTile + 1 +
+                           s2::kDecodeGap);
   const int grid = static_cast<int>(std::min<long long>(std::min(num_sms, s2::kDecodeMaxCtas), tiles));
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_decode<64>(p, grid, sm) : launch_decode<128>(p, grid, sm);

@@ -164,6 +164,33 @@ def test_append_bad_page_and_length_are_reported_and_skipped():
         assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
 
 
+@pytest.mark.parametrize("hq,hkv,d,T", [(2, 1, 128, 5000), (4, 4, 64, 6001), (1, 1, 64, 4736)])
+def test_append_many_tokens_of_few_heads(hq, hkv, d, T):
+    """The form with 32 tokens a block, on views of one packed projection, ragged sequences, some of
+    them empty; rows behind the last sequence untouched."""
+    r = random.Random(T)
+    new = [0]
+    while sum(new) < T - 200:
+        new.append(r.choice([0, 1, 31, 32, 33, 700]))
+    T0, page = sum(new), 40
+    rows, pages = _table(new, page, 4)
+    packed = _randn(8, T, hq + 2 * hkv, d)
+    q, k, v = packed[:, :hq], packed[:, hq:hq + hkv], packed[:, hq + hkv:]
+    kc, vc = _caches(20, pages, page, hkv, d, "kv_by_token")
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    before = packed.clone()
+    s2.s2attn_rope_append(q, q, k, k, v, kc, vc, _ints(rows), _ints(new), _ints(cu), pi_scale=0.5)
+    _ok()
+    pos = torch.tensor([i for n in new for i in range(n)], device="cuda")
+    seq = torch.tensor([s for s, n in enumerate(new) for _ in range(n)], device="cuda")
+    _near_bf16(packed[:T0, :hq + hkv], _turn64(before[:T0, :hq + hkv], pos, 10000.0, 0.5), 1.2e-5)
+    assert torch.equal(packed[T0:], before[T0:]) and torch.equal(v, before[:, hq + hkv:])
+    pg = torch.tensor(rows, device="cuda")[seq, pos // page]
+    assert torch.equal(kc[pg, pos % page], k[:T0]) and torch.equal(vc[pg, pos % page], v[:T0])
+
+
 # ------------------------------------------------------------------------------------------
 # decode
 # ------------------------------------------------------------------------------------------
@@ -210,6 +237,9 @@ DECODE = [
     ([9000], 64, 8, 128, 64, "apart"),             # one long sequence, split over every SM
     ([33] * 300 + [0, 2000], 4, 4, 64, 16, "apart"),   # more sequences than a block has threads
     ([0, 0], 4, 2, 64, 16, "apart"),
+    ([5000, 20000], 8, 8, 128, 64, "apart"),       # segments across warps and CTAs, one row each
+    ([12000], 24, 2, 64, 16, "apart"),             # 12 rows: partials of 16-row warps
+    ([47] * 40 + [4000], 8, 1, 128, 16, "apart"),
 ]
 
 
