@@ -68,7 +68,7 @@ typedef enum {
  * dS hand-off entries and the work counters in the backward workspace; 3 adds the option flags
  * (_general entries, which replace the strided-only entries) and s2attn_rope_pi; 4 adds the
  * _general forms of the two dS hand-off stages; 5 adds s2attn_fwd_rope_q. Entries that were
- * added beside these without changing any of them (s2attn_rope_append, s2attn_decode) leave the
+ * added beside these without changing any of them (the serving entries) leave the
  * version as it is: a caller finds out by looking their symbols up. */
 S2ATTN_API int s2attn_abi_version(void);
 
@@ -356,6 +356,7 @@ S2ATTN_API s2attn_status s2attn_rope_pi(const void* x, void* y, int B, int N, in
  * Serving. The fine-tuned model answers with standard attention over the whole extended context
  * (summary page, §3.2: S²-Attn is used in fine-tuning only), so what follows is full causal
  * attention with rotary positions and a paged key/value cache:
+ *   s2attn_prompt_fwd   attends over whole prompts, packed one after another;
  *   s2attn_rope_append  turns new queries and keys and puts keys and values into the cache;
  *   s2attn_decode       attends from one new token per sequence over the cache.
  *
@@ -419,6 +420,25 @@ S2ATTN_API s2attn_status s2attn_decode(const void* q, const void* k_cache, const
                                        int page_size, int max_pages, float scale,
                                        const long long* strides, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention over packed prompts: the rows of n_seqs sequences follow one another in q, o
+ * bf16 [T, Hq, d] and k, v bf16 [T, Hkv, d]; sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+ * (a HOST array of n_seqs + 1 ints, not decreasing, within [0, T]; lengths of 0 allowed; read during the
+ * call only). Row i of a sequence sees its rows 0..i: o = softmax(scale * q k^T) v, lse fp32 [Hq, T]
+ * (natural log). Query head h reads kv head h / (Hq / Hkv); q and k must be turned already
+ * (s2attn_rope_append with k_rot, s2attn_rope_pi). Rows of no sequence are neither read into a
+ * result nor written. A value row that is not finite may turn the rows before it in its own 128 rows of
+ * the sequence into NaN as well (0 * NaN); it does not reach other sequences.
+ * `strides`: NULL or the row strides of {q, k, v, o}, multiples of 8 and at least heads * d; tensors
+ * must not overlap. T > 2^23 or Hq >= 2^20 -> S2ATTN_ERR_UNSUPPORTED. One launch per 512 sequences and
+ * 2048 query tiles (of 128 rows, or 256 where Hq / Hkv is odd); a captured graph keeps the lengths it was
+ * captured with. Asynchronous on `stream`; allocates no device memory.
+ */
+S2ATTN_API s2attn_status s2attn_prompt_fwd(const void* q, const void* k, const void* v, void* o,
+                                           float* lse, const int* cu_seqlens, int n_seqs, int T,
+                                           int Hq, int Hkv, int d, float scale,
+                                           const long long* strides, void* stream);
 
 #ifdef __cplusplus
 }

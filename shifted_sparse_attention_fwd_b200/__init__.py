@@ -42,6 +42,8 @@ from ._serve import (  # noqa: F401
     s2attn_rope_append,
     s2attn_decode,
     s2attn_decode_workspace_size,
+    s2attn_prompt_fwd,
     rope_append,
     decode,
+    prompt_fwd,
 )

@@ -59,6 +59,7 @@ SIGNATURES = {
     "s2attn_rope_append": (_I, [_P] * 10 + [_I] * 8 + [_F, _F, _P, _P]),
     "s2attn_decode_workspace_size": (_Z, [_I] * 4),
     "s2attn_decode": (_I, [_P] * 7 + [_I] * 7 + [_F, _P, _P, _Z, _P]),
+    "s2attn_prompt_fwd": (_I, [_P] * 6 + [_I] * 5 + [_F, _P, _P]),
     "s2attn_set_wait_timeout_ns": (None, [ctypes.c_ulonglong]),
     "s2attn_selftest_wait_timeout": (_I, [ctypes.c_ulonglong, _P]),
 }

@@ -1,5 +1,5 @@
-"""Binding of the serving entries of libs2attn.so: rotation and append, and decode over a paged
-key/value cache (include/s2attn.h, "Serving").
+"""Binding of the serving entries of libs2attn.so: rotation and append to a paged key/value cache,
+decode over it, and attention over packed prompts (include/s2attn.h, "Serving").
 
 Argument marshalling only, as in _lib.py. A decoding step is a few microseconds of GPU work, so
 these functions keep their own cost low: one pass over the arguments and one ctypes call. Tensors
@@ -159,6 +159,31 @@ def s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale=No
         d ** -0.5 if scale is None else scale, strides, workspace.data_ptr(), workspace.numel()))
 
 
+def s2attn_prompt_fwd(q, k, v, o, lse, cu_seqlens, scale=None, stream=None):
+    """Causal attention over packed prompts: q, o [T,Hq,d], k, v [T,Hkv,d] bf16; lse fp32 [Hq,T].
+    cu_seqlens: the sequences' first rows and the end of the last, on the HOST (a contiguous int32 CPU tensor,
+    or a sequence of ints). Views with contiguous (heads, d) blocks are accepted."""
+    index = q.get_device()
+    T, Hq, d = rows = q.shape
+    Hkv = k.shape[1]
+    kv = (T, Hkv, d)
+    named = (("q", q, rows), ("k", k, kv), ("v", v, kv), ("o", o, rows))
+    strides = None
+    if not _tensors(index, *named):
+        strides = (ctypes.c_longlong * 4)(*(x for name, t, _ in named for x in _outer_strides(name, t)))
+    _check("lse", lse, torch.float32, (Hq, T), index)
+    if not lse.is_contiguous():
+        raise ValueError("lse: expected a contiguous tensor")
+    if not isinstance(cu_seqlens, torch.Tensor):
+        cu_seqlens = torch.tensor(cu_seqlens, dtype=_I32)
+    if (cu_seqlens.is_cuda or cu_seqlens.dtype is not _I32 or cu_seqlens.dim() != 1
+            or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens: expected a contiguous int32 CPU tensor of one axis, or a sequence of ints")
+    _run("s2attn_prompt_fwd", index, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(),
+        cu_seqlens.numel() - 1, T, Hq, Hkv, d, d ** -0.5 if scale is None else scale, strides))
+
+
 # ------------------------------------------------------------------------------------------
 # Allocating conveniences
 # ------------------------------------------------------------------------------------------
@@ -179,4 +204,13 @@ def decode(q, k_cache, v_cache, block_table, cache_lens, scale=None, stream=None
         o = torch.empty_like(q)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale, None, stream)
+    return o, lse
+
+
+def prompt_fwd(q, k, v, cu_seqlens, scale=None, stream=None):
+    """s2attn_prompt_fwd into new tensors: returns (o, lse). Rows of no sequence are left unset."""
+    with _on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    s2attn_prompt_fwd(q, k, v, o, lse, cu_seqlens, scale, stream)
     return o, lse

@@ -1,0 +1,601 @@
+// Causal attention over packed prompts of different lengths (O and row log-sum-exp), sm_100a
+// tensor cores.
+//
+// The sequences' rows follow one another in q, k, v [T, heads, D]; row i of a sequence sees its
+// rows 0..i: o_i = sum_j p_ij v_j / l_i, p_ij = exp(scale q_i . k_j), l_i = sum_j p_ij, lse_i = log l_i.
+// 4 D flops per visible (query head, row, key): bound by the tensor cores, and next to them by
+// the exponentials (2 x 128 x 128 on 16 lanes a cycle are 2048 cycles per step, the step's 32 MMAs 2048
+// to 2750).
+//
+// A work unit is two 128-row query tiles that share their key/value tiles: the same rows of two
+// query heads of one kv head where the group is even (both tiles then see the same keys), or 256
+// consecutive rows of one head. Each CTA (one per SM) goes on to the next unit by cancelling the launch of
+// a block that has not started yet (cluster launch control): units are balanced at run time, in
+// the order of the grid, with no counter in memory. The order is by chunks of kv heads whose K and V
+// fit L2 together, the heaviest query tiles of all sequences first in each chunk.
+//
+// Warp roles (320 threads):
+//   warps 0-3, 4-7  softmax of query tile 0 / 1: thread i owns row i (TMEM lane i), fp32 online
+//                   softmax, P written to TMEM as bf16 over S, epilogue.
+//   warp 8          producer: next unit, TMA loads (Q tiles, K ring, V ring).
+//   warp 9          TMEM allocator and MMA issuer (one lane).
+// TMEM columns: S0/P0 [0,128), S1/P1 [128,256), O0 [256,256+D), O1 [256+D, 256+2D).
+// MMA order: S0(0) S1(0) PV0(0) S0(1) PV1(0) S1(1) ...: one tile's MMAs run beside the other tile's
+// softmax; the next unit's first S0 goes out before the last PV1 if its tiles have landed.
+//
+// Softmax pass: after a tile's first step the exponentials are taken against the running maximum as it
+// stands, while the new maximum is still being found (it must not have grown by more than 2^8, else
+// the pass is repeated from S, which is still in TMEM): the maximum search leaves the critical path.
+//
+// Rows of other sequences in a tile: their keys are masked; their values, whatever they hold
+// (0 * NaN), never reach a product: the last V tile of a sequence is loaded without them.
+#pragma once
+
+#include "s2_common.cuh"
+#include "s2_serve_common.cuh"
+#include "s2_tmem_wide.cuh"
+
+namespace s2 {
+
+constexpr int kPromptMaxSeqs = 512;       // sequences and query tiles of one launch
+constexpr int kPromptMaxTiles = 2048;
+
+struct PromptParams {
+  const __nv_bfloat16* v;
+  long long v_st;
+  __nv_bfloat16* o;
+  long long o_st;
+  float* lse;                             // [Hq, T]
+  int T, Hq, Hkv, group;
+  int n_tiles, kv_chunk;                  // entries of `tile`; kv heads taken together
+  float scale_log2;
+  unsigned int* err;
+  unsigned long long timeout_ns;
+};
+// What the host lays out for one launch: the sequences, and their query tiles (128 or 256 rows), the
+// heaviest first: sequence << 16 | tile.
+struct PromptWork {
+  int start[kPromptMaxSeqs], len[kPromptMaxSeqs];
+  unsigned int tile[kPromptMaxTiles];
+};
+
+// One unit as the roles read it from the ring.
+struct PromptUnit {
+  int live;                               // 0: no unit is left
+  int kvh, h[2];
+  int start, len;                         // the sequence's rows
+  int qt[2], n[2];                        // query tile of 128 rows, and its key tiles (0: no such tile)
+};
+
+template <int D>
+struct PromptLayout {
+  static constexpr uint32_t kTile = Tile<D>::kBytes;
+  static constexpr int kStages = 2;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kTile;
+  static constexpr uint32_t kV = kK + kStages * kTile;
+  static constexpr uint32_t kStageWarp = 32 * 128;          // O staging: 32 rows x 64 columns
+  static constexpr uint32_t kStage = kV + kStages * kTile;
+  static constexpr uint32_t kClc = kStage + 8 * kStageWarp; // response of the launch control, 16 bytes
+  static constexpr uint32_t kRing = kClc + 16;
+  enum { B_Q = 0, B_QE = 2, B_K = 4, B_KE = B_K + kStages, B_V = B_KE + kStages, B_VE = B_V + kStages,
+         B_S = B_VE + kStages, B_P = B_S + 2, B_ODONE = B_P + 2, B_UF = B_ODONE + 2,
+         B_UE = B_UF + kUnitRing, B_CLC = B_UE + kUnitRing, B_DRAIN, B_COUNT };
+  static constexpr uint32_t kBar = (kRing + kUnitRing * sizeof(PromptUnit) + 7) / 8 * 8;
+  static constexpr uint32_t kTmemSlot = kBar + B_COUNT * 8;
+  static constexpr uint32_t kAbort = kTmemSlot + 4;
+  static constexpr uint32_t kBytes = kAbort + 4;
+  // (at least 116 KB, so that one CTA is resident per SM: each takes all of TMEM)
+  static constexpr uint32_t kLaunchBytes = kBytes + 1024 > 116 * 1024 ? kBytes + 1024 : 116 * 1024;
+  static constexpr int kThreads = 320;
+  static_assert(kLaunchBytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+// Cluster launch control: ask for a block that has not started; 16 bytes arrive at `dst`, counted on
+// `bar`. After an answer without a block no further request may follow.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// The block's x index, or -1.
+__device__ __forceinline__ int clc_answer(uint32_t src) {
+  int x, got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.s32 %1, 1, 0, p;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, a;\n\t}"
+      : "=r"(x), "=r"(got)
+      : "r"(src)
+      : "memory");
+  return got ? x : -1;
+}
+
+// kHeads: the unit's two tiles are two heads' same rows (else 256 rows of one head).
+template <bool kHeads>
+__device__ __forceinline__ PromptUnit prompt_unit(const PromptParams& p, const PromptWork& w, int u) {
+  const int per_kv = kHeads ? p.group / 2 : p.group;
+  const int full = p.kv_chunk * per_kv * p.n_tiles;
+  const int kv0 = u / full * p.kv_chunk;
+  const int in = u % full, here = min(p.kv_chunk, p.Hkv - kv0) * per_kv;
+  const int head = in % here;
+  const unsigned int e = w.tile[in / here];
+  PromptUnit r;
+  r.live = 1;
+  r.kvh = kv0 + head / per_kv;
+  const int h0 = r.kvh * p.group + (head % per_kv) * (kHeads ? 2 : 1);
+  r.h[0] = h0;
+  r.h[1] = kHeads ? h0 + 1 : h0;
+  r.start = w.start[e >> 16];
+  r.len = w.len[e >> 16];
+  const int t = static_cast<int>(e & 0xFFFFu);
+  r.qt[0] = kHeads ? t : 2 * t;
+  r.qt[1] = kHeads ? t : 2 * t + 1;
+  r.n[0] = r.qt[0] + 1;
+  r.n[1] = r.qt[1] * kTileRows < r.len ? r.qt[1] + 1 : 0;
+  return r;
+}
+
+// Tensor memory loads whose results may be used after tmem_ld_done.
+#define S2_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
+                 "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : S2_R8(0), S2_R8(8), S2_R8(16), S2_R8(24)
+      : "r"(taddr)
+      : "memory");
+}
+#undef S2_R8
+#define S2_U8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+                 "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : S2_U8(0), S2_U8(8), S2_U8(16), S2_U8(24)::"memory");
+}
+#undef S2_U8
+
+// 32 scores of a row: P = exp2(c s - m) as bf16 pairs into pk, the sums into acc, the largest score
+// (of s, not scaled) into mx. Scores behind column `lim` are masked.
+template <bool kMask>
+__device__ __forceinline__ void softmax32(const uint32_t (&r)[32], int lim, uint64_t c2, uint64_t nm2,
+                                          uint32_t* pk, uint64_t (&acc)[2], float (&mx)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float s0 = __uint_as_float(r[2 * i]), s1 = __uint_as_float(r[2 * i + 1]);
+    if (kMask) {
+      s0 = 2 * i > lim ? -INFINITY : s0;
+      s1 = 2 * i + 1 > lim ? -INFINITY : s1;
+    }
+    mx[i & 1] = max3f(mx[i & 1], s0, s1);
+    const uint64_t a = f2_fma(f2_pack(s0, s1), c2, nm2);
+    const float e0 = fast_exp2(f2_lo(a)), e1 = fast_exp2(f2_hi(a));
+    acc[i & 1] = f2_add(acc[i & 1], f2_pack(e0, e1));
+    pk[i] = pack_bf16(e0, e1);
+  }
+}
+
+template <int D, bool kHeads>
+__global__ void __launch_bounds__(320, 1)
+    s2_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV8,
+                     const __grid_constant__ CUtensorMap tmO8, const __grid_constant__ PromptParams p,
+                     const __grid_constant__ PromptWork work) {
+  using L = PromptLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = aligned_smem(smem_raw);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto bar = [&](int i) { return sbase + L::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  PromptUnit* ring = reinterpret_cast<PromptUnit*>(smem + L::kRing);
+  const WaitCtx ctx{abort_flag, p.err, p.timeout_ns, KID_PROMPT};
+
+  if (warp == 8 && lane == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L::B_Q + s), 1);
+      mbar_init(bar(L::B_QE + s), 1);
+      mbar_init(bar(L::B_S + s), 1);
+      mbar_init(bar(L::B_P + s), 4);
+      mbar_init(bar(L::B_ODONE + s), 1);
+    }
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(bar(L::B_K + s), 1);
+      mbar_init(bar(L::B_KE + s), 1);
+      mbar_init(bar(L::B_V + s), 1);
+      mbar_init(bar(L::B_VE + s), 1);
+    }
+    for (int s = 0; s < kUnitRing; ++s) {
+      mbar_init(bar(L::B_UF + s), 1);
+      mbar_init(bar(L::B_UE + s), 9);     // the eight softmax warps and the MMA thread
+    }
+    mbar_init(bar(L::B_CLC), 1);
+    mbar_init(bar(L::B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+    tma_prefetch_map(&tmO8);
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The k-th unit of this CTA, for a whole warp or one thread.
+  auto read_rec = [&](int k, PromptUnit& u, bool whole_warp, uint32_t site) -> bool {
+    const int slot = k % kUnitRing;
+    bool ok = wait_bar(bar(L::B_UF + slot), (k / kUnitRing) & 1, ctx, site);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    u = ring[slot];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(bar(L::B_UE + slot));
+    return u.live != 0;
+  };
+
+  if (warp == 8) {
+    // ---------------- producer (the whole warp; lane 0 issues) ----------------
+    int k_issued = 0, v_issued = 0, q_loads[2] = {0, 0};
+    int clc_asked = -1;                   // the open request's number
+    bool ok = true;
+    PromptUnit u = prompt_unit<kHeads>(p, work, blockIdx.x);
+    auto load_box = [&](uint32_t dst, const CUtensorMap* m, int b, int h, int row) {
+      if (lane == 0) {
+        mbar_expect_tx(bar(b), Tile<D>::kBytes);
+#pragma unroll
+        for (int half = 0; half < Tile<D>::kHalves; ++half)
+          tma_load_4d(dst + half * Tile<D>::kHalfBytes, m, bar(b), half * 64, h, row, 0);
+      }
+      __syncwarp();
+    };
+    auto issue_k = [&](int j) -> bool {
+      const int i = k_issued, st = i % L::kStages;
+      if (i >= L::kStages && !warp_wait(bar(L::B_KE + st), ((i / L::kStages) - 1) & 1, ctx, 1)) return false;
+      load_box(sbase + L::kK + st * L::kTile, &tmK, L::B_K + st, u.kvh, u.start + j * kTileRows);
+      ++k_issued;
+      return true;
+    };
+    auto issue_v = [&](int j) -> bool {
+      const int i = v_issued, st = i % L::kStages;
+      if (i >= L::kStages && !warp_wait(bar(L::B_VE + st), ((i / L::kStages) - 1) & 1, ctx, 2)) return false;
+      const uint32_t dst = sbase + L::kV + st * L::kTile;
+      const int valid = u.len - j * kTileRows, row0 = u.start + j * kTileRows;
+      if (valid >= kTileRows) {
+        load_box(dst, &tmV, L::B_V + st, u.kvh, row0);
+      } else {
+        // The sequence ends inside the tile: whole 8-row atoms by TMA, the one that the end cuts by
+        // the warp's own copies, and zeros (rows out of the tensor's bounds) behind it.
+        const int whole = valid / 8, cut = valid % 8;
+        if (cut) {
+          constexpr int kChunks = D / 8;
+          for (int x = lane; x < 8 * kChunks; x += 32) {
+            const int r = x / kChunks, c = x % kChunks, row = 8 * whole + r;
+            cp_async16(dst + (c / 8) * Tile<D>::kHalfBytes + row * 128 + (((c % 8) ^ (row & 7)) * 16),
+                       p.v + (row0 + (r < cut ? row : 0)) * p.v_st + static_cast<long long>(u.kvh) * D + 8 * c,
+                       r < cut ? 16u : 0u);
+          }
+          cp_async_wait_all();
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          mbar_expect_tx(bar(L::B_V + st), Tile<D>::kBytes - (cut ? 8 * 128 * Tile<D>::kHalves : 0));
+          for (int a = 0; a < kTileRows / 8; ++a) {
+            if (cut && a == whole) continue;
+#pragma unroll
+            for (int half = 0; half < Tile<D>::kHalves; ++half)
+              tma_load_4d(dst + half * Tile<D>::kHalfBytes + a * 1024, &tmV8, bar(L::B_V + st), half * 64, u.kvh,
+                          a < whole ? row0 + 8 * a : p.T, 0);
+          }
+        }
+        __syncwarp();
+      }
+      ++v_issued;
+      return true;
+    };
+    auto publish = [&](int k) -> bool {
+      const int slot = k % kUnitRing;
+      if (k >= kUnitRing && !warp_wait(bar(L::B_UE + slot), ((k / kUnitRing) - 1) & 1, ctx, 3)) return false;
+      if (lane == 0) {
+        ring[slot] = u;
+        mbar_arrive(bar(L::B_UF + slot));
+      }
+      __syncwarp();
+      return true;
+    };
+    ok = publish(0);
+    for (int k = 0; ok && u.live; ++k) {
+      if (lane == 0) {                    // ask for the next unit
+        mbar_expect_tx(bar(L::B_CLC), 16);
+        clc_request(sbase + L::kClc, bar(L::B_CLC));
+      }
+      clc_asked = k;
+      __syncwarp();
+      const int n = max(u.n[0], u.n[1]);
+      ok = issue_k(0);
+      for (int t = 0; ok && t < 2; ++t) {
+        if (u.n[t] == 0) continue;
+        if (q_loads[t] > 0 && !warp_wait(bar(L::B_QE + t), (q_loads[t] - 1) & 1, ctx, 4)) {
+          ok = false;
+          break;
+        }
+        load_box(sbase + L::kQ + t * L::kTile, &tmQ, L::B_Q + t, u.h[t], u.start + u.qt[t] * kTileRows);
+        ++q_loads[t];
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) ok = issue_k(j + 1);
+        if (ok) ok = issue_v(j);
+      }
+      if (!ok || !warp_wait(bar(L::B_CLC), k & 1, ctx, 5)) {
+        ok = false;
+        break;
+      }
+      clc_asked = -1;
+      const int next = clc_answer(sbase + L::kClc);
+      __syncwarp();
+      fence_async_smem();                 // read before the next request may write
+      if (next >= 0) u = prompt_unit<kHeads>(p, work, next);
+      else u.live = 0;
+      ok = publish(k + 1);
+    }
+    // Every issued copy lands before the CTA can exit.
+    for (int t = 0; t < 2; ++t)
+      if (q_loads[t] > 0) drain_wait(bar(L::B_Q + t), (q_loads[t] - 1) & 1, p.timeout_ns);
+    for (int i = k_issued - L::kStages; i < k_issued; ++i)
+      if (i >= 0) drain_wait(bar(L::B_K + i % L::kStages), (i / L::kStages) & 1, p.timeout_ns);
+    for (int i = v_issued - L::kStages; i < v_issued; ++i)
+      if (i >= 0) drain_wait(bar(L::B_V + i % L::kStages), (i / L::kStages) & 1, p.timeout_ns);
+    if (clc_asked >= 0) drain_wait(bar(L::B_CLC), clc_asked & 1, p.timeout_ns);
+  } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+      int k0 = 0, q_used[2] = {0, 0}, pcount[2] = {0, 0};
+      bool ok = true, early = false;      // early: this unit's first S0 went out during the last unit
+      auto k_slot = [&](int i) { return sbase + L::kK + (i % L::kStages) * L::kTile; };
+      auto wait_k = [&](int i) { return wait_bar(bar(L::B_K + i % L::kStages), (i / L::kStages) & 1, ctx, 7); };
+      auto issue_s = [&](int t, int i) {
+        tc_fence_after();
+        gemm_ss_k<D>(tmem + t * 128, sbase + L::kQ + t * L::kTile, k_slot(i), idesc_qk);
+        mma_commit(bar(L::B_S + t));
+      };
+      for (int ku = 0; ok; ++ku) {
+        PromptUnit u;
+        if (!read_rec(ku, u, false, 6)) break;
+        const int n = max(u.n[0], u.n[1]);
+        if (!wait_k(k0)) break;
+        for (int t = 0; ok && t < 2; ++t) {
+          if (u.n[t] == 0) continue;
+          if (t != 0 || !early) {
+            if (!wait_bar(bar(L::B_Q + t), q_used[t] & 1, ctx, 8)) { ok = false; break; }
+            ++q_used[t];
+            issue_s(t, k0);
+          }
+          if (u.n[t] == 1) mma_commit(bar(L::B_QE + t));   // last S on Q_t
+        }
+        early = false;
+        if (!ok) break;
+        mma_commit(bar(L::B_KE + k0 % L::kStages));
+        for (int j = 0; ok && j < n; ++j) {
+          const int vi = k0 + j, vst = vi % L::kStages;
+          const bool next = j + 1 < n;
+          bool v_ready = false, k_ready = false;
+          for (int t = 0; ok && t < 2; ++t) {
+            if (j < u.n[t]) {
+              if (!wait_bar(bar(L::B_P + t), pcount[t] & 1, ctx, 9)) { ok = false; break; }
+              ++pcount[t];
+              if (!v_ready && !wait_bar(bar(L::B_V + vst), (vi / L::kStages) & 1, ctx, 10)) { ok = false; break; }
+              v_ready = true;
+              tc_fence_after();
+              gemm_ts_mn<D>(tmem + 256 + t * D, tmem + t * 128, sbase + L::kV + vst * L::kTile, idesc_pv, j > 0);
+              if (j + 1 == u.n[t]) mma_commit(bar(L::B_ODONE + t));
+            }
+            if (t == 1) mma_commit(bar(L::B_VE + vst));    // V(j) has no reader left
+            if (j + 1 < u.n[t]) {
+              if (!k_ready && !wait_k(k0 + j + 1)) { ok = false; break; }
+              k_ready = true;
+              issue_s(t, k0 + j + 1);
+              if (j + 2 == u.n[t]) mma_commit(bar(L::B_QE + t));
+            }
+            if (t == 0 && !next) {
+              // The next unit's first S0 before this unit's last PV1, if all it needs is there.
+              const int kn = k0 + n, slot = (ku + 1) % kUnitRing;
+              if (mbar_test_wait(bar(L::B_UF + slot), ((ku + 1) / kUnitRing) & 1) &&
+                  reinterpret_cast<volatile PromptUnit*>(ring)[slot].live &&
+                  mbar_test_wait(bar(L::B_Q), q_used[0] & 1) &&
+                  mbar_test_wait(bar(L::B_K + kn % L::kStages), (kn / L::kStages) & 1)) {
+                ++q_used[0];
+                issue_s(0, kn);
+                early = true;
+              }
+            }
+          }
+          if (ok && next) mma_commit(bar(L::B_KE + (k0 + j + 1) % L::kStages));
+        }
+        k0 += n;
+      }
+    }
+  } else {
+    // ---------------- softmax warps ----------------
+    const int wg = warp / 4;
+    const int row = threadIdx.x % 128;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t s_col = t_lane + wg * 128;
+    const uint32_t o_col = t_lane + 256 + wg * D;
+    const float c = p.scale_log2;
+    const uint64_t c2 = f2_pack(c, c);
+    int s_cnt = 0, o_cnt = 0;
+    bool ok = true;
+    for (int ku = 0; ok; ++ku) {
+      PromptUnit u;
+      if (!read_rec(ku, u, true, 11)) break;
+      const int n = u.n[wg];
+      if (n == 0) continue;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n; ++j, ++s_cnt) {
+        if (!warp_wait(bar(L::B_S + wg), s_cnt & 1, ctx, 12)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t pk[64];
+        uint64_t acc[2] = {0, 0};
+        bool exact = j == 0 || j + 1 == n;           // the first tile, and the diagonal one
+        if (!exact) {
+          const uint64_t nm2 = f2_pack(-m_run, -m_run);
+          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t a[32], b[32];
+          tmem_ld32_begin(s_col, a);
+          tmem_ld_done(a);
+          tmem_ld32_begin(s_col + 32, b);
+          softmax32<false>(a, 0, c2, nm2, pk, acc, mx);
+          tmem_ld_done(b);
+          tmem_ld32_begin(s_col + 64, a);
+          softmax32<false>(b, 0, c2, nm2, pk + 16, acc, mx);
+          tmem_ld_done(a);
+          tmem_ld32_begin(s_col + 96, b);
+          softmax32<false>(a, 0, c2, nm2, pk + 32, acc, mx);
+          tmem_ld_done(b);
+          softmax32<false>(b, 0, c2, nm2, pk + 48, acc, mx);
+          // (a maximum of -inf: the row has seen nothing finite, which the exact pass handles)
+          const bool need = fmaxf(mx[0], mx[1]) * c > m_run + 8.f || m_run == -INFINITY;
+          exact = __any_sync(0xffffffffu, need);
+        }
+        if (exact) {
+          const int lim = j + 1 == n ? row : kTileRows;   // the last tile is the diagonal one
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a[32];
+            tmem_ld32_begin(s_col + 32 * q, a);
+            tmem_ld_done(a);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float s0 = 32 * q + i > lim ? -INFINITY : __uint_as_float(a[i]);
+              const float s1 = 32 * q + i + 1 > lim ? -INFINITY : __uint_as_float(a[i + 1]);
+              mx = max3f(mx, s0, s1);
+            }
+          }
+          const float m_cand = fmaxf(m_run, mx * c);
+          if (__any_sync(0xffffffffu, m_cand > m_run + 8.f)) {
+            // 0 when m_run = -inf; 1 for a row whose scores are all -inf so far
+            const float alpha = m_cand == -INFINITY ? 1.f : fast_exp2(m_run - m_cand);
+            if (j > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t ov[32];
+                tmem_ld32(o_col + 32 * q, ov);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                tmem_st32(o_col + 32 * q, ov);
+              }
+            }
+            l_run *= alpha;
+            m_run = m_cand;
+          }
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t nm2 = f2_pack(-m_use, -m_use);
+          float unused[2] = {0.f, 0.f};
+          acc[0] = acc[1] = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a[32];
+            tmem_ld32_begin(s_col + 32 * q, a);
+            tmem_ld_done(a);
+            softmax32<true>(a, lim - 32 * q, c2, nm2, pk + 16 * q, acc, unused);
+          }
+        }
+        tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+        acc[0] = f2_add(acc[0], acc[1]);
+        l_run += f2_lo(acc[0]) + f2_hi(acc[0]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_P + wg));
+      }
+      if (!ok || !warp_wait(bar(L::B_ODONE + wg), o_cnt & 1, ctx, 13)) { ok = false; break; }
+      ++o_cnt;
+      tc_fence_after();
+      // Epilogue: O / l in bf16 through this warp's staging area (128-byte-swizzled rows of 64
+      // columns): atoms of 8 rows inside the sequence go out as TMA boxes, the rows of the atom that
+      // the sequence's end cuts as row stores, and rows behind the end not at all.
+      const float inv_l = 1.f / l_run;
+      uint8_t* stage = smem + L::kStage + warp * L::kStageWarp;
+      const uint32_t stage_s = sbase + L::kStage + warp * L::kStageWarp;
+      const int r_warp = u.qt[wg] * kTileRows + (warp % 4) * 32;
+      const int left = u.len - r_warp;               // rows of this warp inside the sequence
+      const int tok = u.start + r_warp;
+#pragma unroll 1
+      for (int half = 0; half < D / 64; ++half) {
+        if (lane == 0) bulk_wait_read_all();         // the boxes sent before have been read out
+        __syncwarp();
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          uint32_t ov[32];
+          tmem_ld32(o_col + 64 * half + 32 * q2, ov);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 w4;
+            w4.x = pack_bf16(__uint_as_float(ov[8 * v + 0]) * inv_l, __uint_as_float(ov[8 * v + 1]) * inv_l);
+            w4.y = pack_bf16(__uint_as_float(ov[8 * v + 2]) * inv_l, __uint_as_float(ov[8 * v + 3]) * inv_l);
+            w4.z = pack_bf16(__uint_as_float(ov[8 * v + 4]) * inv_l, __uint_as_float(ov[8 * v + 5]) * inv_l);
+            w4.w = pack_bf16(__uint_as_float(ov[8 * v + 6]) * inv_l, __uint_as_float(ov[8 * v + 7]) * inv_l);
+            const int chunk = 4 * q2 + v;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) * 16)) = w4;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            if (8 * a + 8 <= left) tma_store_4d(&tmO8, stage_s + a * 1024, 64 * half, u.h[wg], tok + 8 * a, 0);
+          bulk_commit();
+        }
+        if (left > 0 && left < 32 && (left & 7) != 0) {
+          const int rr0 = left & ~7;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = rr0 + 4 * i + (lane >> 3), chunk = lane & 7;
+            if (rr < left)
+              *reinterpret_cast<uint4*>(p.o + (tok + rr) * p.o_st + static_cast<long long>(u.h[wg]) * D + 64 * half +
+                                        8 * chunk) =
+                  *reinterpret_cast<const uint4*>(stage + rr * 128 + ((chunk ^ (rr & 7)) * 16));
+          }
+        }
+        __syncwarp();
+      }
+      if (lane < left)
+        p.lse[static_cast<long long>(u.h[wg]) * p.T + tok + lane] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+      tc_fence_before();                  // O is read: the next PV on it waits for this warp's P
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  // ---------------- teardown ----------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    if (lane == 0) {
+      mma_commit(bar(L::B_DRAIN));
+      drain_wait(bar(L::B_DRAIN), 0, p.timeout_ns);
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace s2

@@ -1,4 +1,4 @@
-// Host side of the serving entries of the C ABI (rotation and append, decode): argument
+// Host side of the serving entries of the C ABI (rotation and append, decode, prompts): argument
 // validation and kernel launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <vector>
 
 // s2_device.cuh defines this one function out of line; the library's other translation unit has
 // it under its own name.
@@ -17,6 +18,7 @@
 #include "s2_append.cuh"
 #include "s2_decode.cuh"
 #include "s2_host.h"
+#include "s2_prompt.cuh"
 
 namespace {
 
@@ -33,11 +35,17 @@ ServeDevice g_serve_dev[kMaxDevices];
 
 template <int D>
 cudaError_t serve_smem_attrs() {
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       s2::s2_decode_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2::DecodeLayout<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(s2::s2_decode_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              s2::DecodeLayout<D>::kBytes);
+  e = cudaFuncSetAttribute(s2::s2_decode_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           s2::DecodeLayout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(s2::s2_prompt_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           s2::PromptLayout<D>::kLaunchBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(s2::s2_prompt_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              s2::PromptLayout<D>::kLaunchBytes);
 }
 
 // The error word and SM count of the current device, with the serving kernels set up on it.
@@ -163,6 +171,79 @@ s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t st
   return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_decode_join_kernel launch");
 }
 
+// Tensor map over the rows of a packed bf16 [T, H, d] tensor: dims (d, H, T, 1), box (64, 1, rows, 1),
+// 128-byte swizzle, zeros out of bounds.
+s2attn_status encode_rows(CUtensorMap* m, const void* base, int T, int H, int d, int box_rows, long long st) {
+  const auto encode = s2host::encoder();
+  if (!encode) return S2ATTN_ERR_CUDA;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, 1};
+  cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)st * 2, (cuuint64_t)st * 2 * T};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? S2ATTN_OK : s2host::fail(S2ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
+// K and V of the kv heads that are taken together stay below this: half of L2.
+constexpr long long kPromptL2Bytes = 64ll << 20;
+
+// One launch per kPromptMaxSeqs sequences and kPromptMaxTiles query tiles.
+template <int D>
+s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[5], const int* cu, int n_seqs,
+                            cudaStream_t stream) {
+  static thread_local s2::PromptWork work;
+  static thread_local std::vector<int> order;
+  const bool heads = p.group % 2 == 0;
+  const int rows = heads ? s2::kTileRows : 2 * s2::kTileRows, per_kv = heads ? p.group / 2 : p.group;
+  order.clear();
+  for (int i = 0; i < n_seqs; ++i)
+    if (cu[i + 1] > cu[i]) order.push_back(i);
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int a, int b) { return cu[a + 1] - cu[a] > cu[b + 1] - cu[b]; });
+  auto launch = [&]() -> s2attn_status {
+    const unsigned grid = static_cast<unsigned>(p.Hkv) * per_kv * p.n_tiles;
+    if (heads)
+      s2::s2_prompt_kernel<D, true><<<grid, s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes,
+                                      stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p, work);
+    else
+      s2::s2_prompt_kernel<D, false><<<grid, s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes,
+                                       stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p, work);
+    p.n_tiles = 0;
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_prompt_kernel launch");
+  };
+  for (size_t at = 0; at < order.size(); at += s2::kPromptMaxSeqs) {
+    const int count = static_cast<int>(std::min<size_t>(s2::kPromptMaxSeqs, order.size() - at));
+    long long tokens = 0;
+    for (int i = 0; i < count; ++i) {
+      const int s = order[at + i];
+      work.start[i] = cu[s];
+      work.len[i] = cu[s + 1] - cu[s];
+      tokens += work.len[i];
+    }
+    p.kv_chunk = static_cast<int>(std::max(1ll, std::min<long long>(p.Hkv, kPromptL2Bytes / (tokens * 4 * D))));
+    p.n_tiles = 0;
+    int live = 0;   // the sequences (longest first) that have a tile t
+    for (int t = (work.len[0] - 1) / rows; t >= 0; --t) {
+      while (live < count && (work.len[live] - 1) / rows >= t) ++live;
+      for (int i = 0; i < live; ++i) {
+        work.tile[p.n_tiles++] = static_cast<unsigned>(i) << 16 | static_cast<unsigned>(t);
+        if (p.n_tiles == s2::kPromptMaxTiles) {
+          const s2attn_status s = launch();
+          if (s != S2ATTN_OK) return s;
+        }
+      }
+    }
+    if (p.n_tiles > 0) {
+      const s2attn_status s = launch();
+      if (s != S2ATTN_OK) return s;
+    }
+  }
+  return S2ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -278,6 +359,49 @@ s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_ca
   const int grid = static_cast<int>(std::min<long long>(std::min(num_sms, s2::kDecodeMaxCtas), tiles));
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_decode<64>(p, grid, sm) : launch_decode<128>(p, grid, sm);
+}
+
+s2attn_status s2attn_prompt_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                                const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv, int d,
+                                float scale, const long long* strides, void* stream) {
+  if (!q || !k || !v || !o || !lse || !cu_seqlens) return S2ATTN_ERR_INVALID_ARG;
+  const void* ptrs[4] = {q, k, v, o};
+  for (const void* x : ptrs)
+    if (!aligned16(x)) return S2ATTN_ERR_INVALID_ARG;
+  if (n_seqs <= 0 || T <= 0 || !(scale > 0.f) || !std::isfinite(scale)) return S2ATTN_ERR_INVALID_ARG;
+  s2attn_status s = check_heads(Hq, Hkv, d);
+  if (s != S2ATTN_OK) return s;
+  // units of one launch are counted, and query tiles of a sequence numbered, in 31 and 16 bits
+  if (Hq >= (1 << 20) || T > (1 << 23)) return S2ATTN_ERR_UNSUPPORTED;
+  if (cu_seqlens[0] < 0 || cu_seqlens[n_seqs] > T) return S2ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < n_seqs; ++i)
+    if (cu_seqlens[i + 1] < cu_seqlens[i]) return S2ATTN_ERR_INVALID_ARG;
+  const int head_count[4] = {Hq, Hkv, Hkv, Hq};
+  long long st[4];   // q, k, v, o
+  for (int i = 0; i < 4; ++i) {
+    st[i] = strides ? strides[i] : static_cast<long long>(head_count[i]) * d;
+    if (bad_row_stride(st[i], head_count[i], d)) return S2ATTN_ERR_INVALID_ARG;
+  }
+  CUtensorMap maps[5];
+  if ((s = encode_rows(&maps[0], q, T, Hq, d, s2::kTileRows, st[0])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[1], k, T, Hkv, d, s2::kTileRows, st[1])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[2], v, T, Hkv, d, s2::kTileRows, st[2])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[3], v, T, Hkv, d, 8, st[2])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[4], o, T, Hq, d, 8, st[3])) != S2ATTN_OK) return s;
+  s2::PromptParams p{};
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.v_st = st[2];
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_st = st[3];
+  p.lse = lse;
+  p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.group = Hq / Hkv;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = s2host::wait_timeout_ns();
+  int num_sms = 0;
+  if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
+  cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_prompt<64>(p, maps, cu_seqlens, n_seqs, sm)
+                 : launch_prompt<128>(p, maps, cu_seqlens, n_seqs, sm);
 }
 
 }  // extern "C"

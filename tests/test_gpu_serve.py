@@ -337,3 +337,124 @@ def test_append_then_decode_as_a_model_answers():
                 p = torch.softmax(s, 0)
                 _near_bf16(o[b, h], p @ vv[:, h // 4], (BF16_STEP + 1e-5) * (p @ vv[:, h // 4].abs()))
                 assert abs(float(lse[b, h]) - float(torch.logsumexp(s, 0))) <= 2e-5
+
+
+# ------------------------------------------------------------------------------------------
+# prompts
+# ------------------------------------------------------------------------------------------
+def _prompt64(q, k, v, cu, scale):
+    """o, lse and sum p |v| / sum p in 64 bits, sequence by sequence."""
+    T, hq, d = q.shape
+    g = hq // k.shape[1]
+    o = torch.zeros(T, hq, d, dtype=torch.float64, device="cuda")
+    mean_abs, lse = torch.zeros_like(o), torch.zeros(hq, T, dtype=torch.float64, device="cuda")
+    for a, e in zip(cu, cu[1:]):
+        mask = torch.ones(e - a, e - a, dtype=torch.bool, device="cuda").triu(1)
+        for h in range(hq if e > a else 0):
+            s = (q[a:e, h].double() @ k[a:e, h // g].double().T) * scale
+            s = s.masked_fill(mask, float("-inf"))
+            lse[h, a:e] = torch.logsumexp(s, -1)
+            p = torch.exp(s - lse[h, a:e, None])
+            vv = v[a:e, h // g].double()
+            o[a:e, h], mean_abs[a:e, h] = p @ vv, p @ vv.abs()
+    return o, lse, mean_abs
+
+
+def _cu(lens, first=0):
+    cu = [first]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+PROMPT = [
+    # lens, Hq, Hkv, d, rows before the first sequence, rows behind the last
+    ([1], 1, 1, 64, 0, 0),
+    ([113], 4, 4, 64, 0, 0),
+    ([128], 2, 2, 128, 0, 0),
+    ([129], 2, 2, 128, 0, 0),
+    ([256, 257], 3, 3, 128, 0, 0),
+    ([5, 127, 128, 0, 1, 300, 0, 17], 4, 2, 128, 3, 9),
+    ([700, 8, 641], 8, 1, 64, 0, 130),
+    ([1000, 385], 6, 2, 128, 1, 0),                # an odd group: 256 rows of one head
+    ([2100], 2, 1, 128, 0, 0),
+    ([2500, 31], 1, 1, 64, 0, 1),
+    ([3] * 600 + [150], 2, 2, 64, 0, 0),           # more sequences than one launch takes
+    ([640] * 9, 16, 8, 128, 0, 5),                 # more units than SMs: blocks taken over
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,before,behind", PROMPT)
+@pytest.mark.parametrize("packed", [False, True])
+def test_prompt_matches_formula(lens, hq, hkv, d, before, behind, packed):
+    cu = _cu(lens, before)
+    T = cu[-1] + behind
+    if packed:
+        qkv = _randn(T, T, hq + 2 * hkv, d)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    else:
+        q, k, v = (_randn(T + i, T, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    q *= 2
+    # rows of no sequence hold anything and are left alone
+    for t in (q, k, v):
+        t[:before] = float("nan")
+        t[cu[-1]:] = float("inf")
+    o = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hq, T), 7.0, device="cuda")
+    s2.s2attn_prompt_fwd(q, k, v, o, lse, cu)
+    _ok()
+    want, want_lse, mean_abs = _prompt64(q, k, v, cu, d ** -0.5)
+    a, e = cu[0], cu[-1]
+    _near_bf16(o[a:e], want[a:e], (BF16_STEP + 1e-5) * mean_abs[a:e])
+    assert float((lse[:, a:e].double() - want_lse[:, a:e]).abs().max()) <= 2e-5
+    assert (o[:a] == 7).all() and (o[e:] == 7).all() and (lse[:, :a] == 7).all() and (lse[:, e:] == 7).all()
+    o2, lse2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    s2.s2attn_prompt_fwd(q, k, v, o2, lse2, torch.tensor(cu, dtype=torch.int32))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (2, 2, 64)])
+def test_prompt_growing_scores_and_other_sequences(hq, hkv, d):
+    """Scores that grow along the keys by far more than 2^8 (the running maximum is rescaled again and
+    again), next to sequences that hold NaN and infinities."""
+    lens = [300, 777, 129, 60]
+    cu = _cu(lens)
+    q, k, v = (_randn(40 + i, cu[-1], h, d) for i, h in enumerate((hq, hkv, hkv)))
+    q[cu[1]:cu[2]] = q[cu[1]:cu[2]].abs()
+    ramp = torch.linspace(0, 12, lens[1], device="cuda")[:, None, None]
+    k[cu[1]:cu[2]] = (k[cu[1]:cu[2]].float() * 0.1 + ramp).to(torch.bfloat16)
+    for t, x in ((q, "nan"), (k, "inf"), (v, "nan")):
+        t[cu[0]:cu[1]] = float(x)
+        t[cu[2]:cu[3]] = float(x)
+    o, lse = s2.prompt_fwd(q, k, v, cu, scale=0.5)
+    _ok()
+    for i in (1, 3):
+        a, e = cu[i], cu[i + 1]
+        want, want_lse, mean_abs = _prompt64(q[a:e], k[a:e], v[a:e], [0, e - a], 0.5)
+        # scores reach 10^3 here, held to 24 bits: products of fp32 sums, 2^-20 relative and 1e-3
+        # absolute in the exponent, which moves the weights by as much
+        big = max(1.0, float(want_lse.abs().max()))
+        _near_bf16(o[a:e], want, (BF16_STEP + 1e-5 + 2 * big * 2 ** -20) * mean_abs)
+        assert float((lse[:, a:e].double() - want_lse).abs().max()) <= 2e-5 + big * 2 ** -20
+
+
+def test_prompt_append_decode_agree():
+    """A prompt through append and prompt_fwd, then its last row again as a decoding step: the same
+    attention from the cache."""
+    hq, hkv, d, page = 8, 2, 128, 32
+    lens = [200, 1, 513]
+    cu = _cu(lens)
+    rows, pages = _table(lens, page, 2)
+    q, k, v = (_randn(70 + i, cu[-1], h, d) for i, h in enumerate((hq, hkv, hkv)))
+    kc, vc = _randn(1, pages, page, hkv, d), _randn(2, pages, page, hkv, d)
+    q_rot, k_rot = s2.rope_append(q, k, v, kc, vc, _ints(rows), _ints(lens), _ints(cu), pi_scale=0.5)
+    o, lse = s2.prompt_fwd(q_rot, k_rot, v, cu)
+    last = torch.tensor(cu[1:], device="cuda") - 1
+    o1, lse1 = s2.decode(q_rot[last], kc, vc, _ints(rows), _ints(lens))
+    _ok()
+    want, want_lse, mean_abs = _prompt64(q_rot, k_rot, v, cu, d ** -0.5)
+    slack = (BF16_STEP + 1e-5) * mean_abs
+    _near_bf16(o, want, slack)
+    _near_bf16(o1, want[last], slack[last])
+    assert float((lse.double() - want_lse).abs().max()) <= 2e-5
+    assert float((lse1.double() - want_lse[:, last].T).abs().max()) <= 2e-5

@@ -79,6 +79,27 @@ def test_decode_workspace(lib):
     assert f(1, 128, 8, 128) < 13 << 20
 
 
+def prompt_call(lib, cu=(0, 100, 100, 256), **kw):
+    import ctypes
+    a = dict(q=A, k=A, v=A, o=A, lse=A, cu=(ctypes.c_int * len(cu))(*cu) if cu else None, n=len(cu or ()) - 1,
+             T=256, Hq=4, Hkv=2, d=64, scale=0.125, strides=None)
+    a.update(kw)
+    return lib.s2attn_prompt_fwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
+    (dict(lse=None), INVALID), (dict(cu=None), INVALID), (dict(q=A + 8), INVALID), (dict(o=A + 2), INVALID),
+    (dict(n=0), INVALID), (dict(T=0), INVALID), (dict(T=255), INVALID), (dict(cu=(-1, 5)), INVALID),
+    (dict(cu=(0, 9, 8, 20)), INVALID), (dict(cu=(0, 300, 200)), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(Hkv=3), INVALID), (dict(d=80), UNSUPPORTED),
+    (dict(T=(1 << 23) + 1), UNSUPPORTED), (dict(Hq=1 << 20, Hkv=1), UNSUPPORTED),
+    (dict(strides=_strides(256, 128, 128, 250)), INVALID), (dict(strides=_strides(256, 120, 128, 256)), INVALID),
+])
+def test_prompt_rejects(lib, kw, status):
+    assert prompt_call(lib, **kw) == status
+
+
 def test_binding_refuses_cpu_tensors_types_and_shapes():
     """The binding checks before it passes addresses on."""
     def t(*shape, dtype=torch.bfloat16):
