@@ -384,8 +384,8 @@ s2attn_status s2attn_prompt_fwd(const void* q, const void* k, const void* v, voi
   }
   CUtensorMap maps[5];
   if ((s = encode_rows(&maps[0], q, T, Hq, d, s2::kTileRows, st[0])) != S2ATTN_OK) return s;
-  if ((s = encode_rows(&maps[1], k, T, Hkv, d, s2::kTileRows, st[1])) != S2ATTN_OK) return s;
-  if ((s = encode_rows(&maps[2], v, T, Hkv, d, s2::kTileRows, st[2])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[1], k, T, Hkv, d, s2::kPromptKeys, st[1])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[2], v, T, Hkv, d, s2::kPromptKeys, st[2])) != S2ATTN_OK) return s;
   if ((s = encode_rows(&maps[3], v, T, Hkv, d, 8, st[2])) != S2ATTN_OK) return s;
   if ((s = encode_rows(&maps[4], o, T, Hq, d, 8, st[3])) != S2ATTN_OK) return s;
   s2::PromptParams p{};
