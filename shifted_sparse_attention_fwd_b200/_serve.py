@@ -7,8 +7,8 @@ that belong to another device than the current one are run on that device's curr
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -19,26 +19,36 @@ _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle
 _get_device = torch._C._cuda_getDevice
 
 
-def _on(stream, device):
-    """What is allocated for a call belongs to the stream that the call runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
+def _owner(stream, device):
+    """Context in which the tensors of a call are allocated: they belong to the stream it runs on."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
 
 
+def _like(t, stream):
+    """A new contiguous tensor of t's shape and type."""
+    if stream is None:
+        return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    with _owner(stream, t.device):
+        return t.new_empty(t.shape)
+
+
+def _new(t, shape, dtype, stream):
+    if stream is None:
+        return t.new_empty(shape, dtype=dtype)
+    with _owner(stream, t.device):
+        return t.new_empty(shape, dtype=dtype)
+
+
 def _run(name, index, stream, args):
     """The C function on device `index`, which is made current, with the stream's handle last."""
-    if stream is None:
-        handle = _raw_stream(index)
-    else:
-        handle = _stream(stream)
+    fn = getattr(lib(), name)
     if index == _get_device():
-        status = getattr(lib(), name)(*args, handle)
+        status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(index):
-            status = getattr(lib(), name)(*args, handle)
+            status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     if status != S2ATTN_OK:
         raise S2AttnError(status, name)
 
@@ -114,6 +124,7 @@ def s2attn_rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cac
         base, pi_scale, strides))
 
 
+@functools.lru_cache(maxsize=256)
 def s2attn_decode_workspace_size(B, Hq, Hkv, d) -> int:
     return int(lib().s2attn_decode_workspace_size(B, Hq, Hkv, d))
 
@@ -141,12 +152,7 @@ def s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale=No
         if not lse.is_contiguous():
             raise ValueError("lse: expected a contiguous tensor")
     if workspace is None:
-        n = s2attn_decode_workspace_size(B, Hq, Hkv, d)
-        if stream is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:
-            with _on(stream, q.device):
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _new(q, s2attn_decode_workspace_size(B, Hq, Hkv, d), torch.uint8, stream)
     else:
         _check("workspace", workspace, torch.uint8, workspace.shape, index)
         if not workspace.is_contiguous():
@@ -191,8 +197,7 @@ def rope_append(q, k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens=N
                 pi_scale=1.0, stream=None):
     """s2attn_rope_append into new tensors: returns (q_rot, k_rot). Rows that are skipped (idle, or
     behind the last sequence) are left unset."""
-    with _on(stream, k.device):
-        q_rot, k_rot = torch.empty_like(q), torch.empty_like(k)
+    q_rot, k_rot = _like(q, stream), _like(k, stream)
     s2attn_rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens,
                        base, pi_scale, stream)
     return q_rot, k_rot
@@ -200,17 +205,13 @@ def rope_append(q, k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens=N
 
 def decode(q, k_cache, v_cache, block_table, cache_lens, scale=None, stream=None):
     """s2attn_decode into new tensors: returns (o, lse)."""
-    with _on(stream, q.device):
-        o = torch.empty_like(q)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    o, lse = _like(q, stream), _new(q, q.shape[:2], torch.float32, stream)
     s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale, None, stream)
     return o, lse
 
 
 def prompt_fwd(q, k, v, cu_seqlens, scale=None, stream=None):
     """s2attn_prompt_fwd into new tensors: returns (o, lse). Rows of no sequence are left unset."""
-    with _on(stream, q.device):
-        o = torch.empty_like(q)
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    o, lse = _like(q, stream), _new(q, (q.shape[1], q.shape[0]), torch.float32, stream)
     s2attn_prompt_fwd(q, k, v, o, lse, cu_seqlens, scale, stream)
     return o, lse

@@ -16,6 +16,8 @@
 // partial results go to the workspace, and a second small kernel, one block per CTA boundary and
 // query row, joins them. Pieces are always added in the list's order, with no atomics: the same
 // bits every time. The second kernel is launched programmatically early and waits on the device.
+// Where the block table holds few tokens a sequence and there are no more segments than SMs, each CTA
+// takes a whole segment instead and the second kernel falls away.
 //
 // A warp is on its own: it copies its tiles' rows to its part of shared memory with 16-byte
 // asynchronous copies (the row's page looked up one tile ahead), kDecodeStages tiles deep, so
@@ -36,6 +38,8 @@ constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kDecodeTile = 16;           // tokens
 constexpr int kDecodeRows = 16;           // query heads a warp takes at a time (one MMA's rows)
 constexpr int kDecodeGap = 1;
+// At most this many tokens a sequence, and no more segments than SMs: a CTA takes a whole segment.
+constexpr int kDecodeWholeTokens = 512;
 constexpr int kDecodeMaxCtas = 148;       // the workspace has room for this many CTAs' partials
 constexpr int kDecodeJoinThreads = 256;
 
@@ -64,6 +68,7 @@ struct DecodeParams {
   const int *table, *lens;
   int B, Hq, Hkv, pages, page_size, max_pages;
   int group, chunks;                      // query heads per kv head, and their chunks of 16
+  int whole;                              // a CTA takes a whole segment
   FastDiv by_page;
   float scale_log2;
   float* first_o;                         // [warps][rows][D]: pieces of a warp's first segment
@@ -111,6 +116,11 @@ __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
 }
 __device__ __forceinline__ int decode_tiles(int len) { return len / kDecodeTile + (len % kDecodeTile != 0); }
 
+template <int N>
+struct IntConst {
+  static constexpr int value = N;
+};
+
 // A tile: its sequence, head, number in the segment, and its place in the list.
 struct DecodeAt {
   int b, hv, tile, tiles, len;            // hv = kv head * chunks + chunk of its query heads
@@ -138,12 +148,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_launch_dependents();
   if (threadIdx.x < 2 * kDecodeWarps) s_piece[threadIdx.x].kind = 0;
+  if (threadIdx.x == 0) p.tail[blockIdx.x].valid = 0;
 
-  // ---- the list: places before every run of `per` sequences ----
   const int hv_count = p.Hkv * p.chunks;
+  // ---- the list: places before every run of `per` sequences ----
   const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;
   auto places = [](int tiles) { return tiles == 0 ? 0 : tiles + kDecodeGap; };   // of one segment
-  {
+  if (!p.whole) {
     long long sum = 0;
     for (int i = 0; i < per; ++i) {
       const int b = threadIdx.x * per + i;
@@ -165,10 +176,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     if (threadIdx.x == 0) s_pre[0] = 0;
     __syncthreads();
   }
-  const long long total = s_pre[kDecodeThreads] * hv_count;
-  const long long cta_range = (total + gridDim.x - 1) / gridDim.x;
-  const long long cta_first = blockIdx.x * cta_range;
-  const long long cta_last = cta_first + cta_range < total ? cta_first + cta_range : total;
+  long long cta_first = 0, cta_last = 0, cta_range;
+  int own_b = 0, own_len = 0;             // of a CTA that takes a whole segment: its places begin at 0
+  if (p.whole) {
+    own_b = blockIdx.x / hv_count;
+    own_len = decode_len(p, own_b);
+    if (threadIdx.x == 0 && own_len != p.lens[own_b]) report_bad_index(p.err, KID_DECODE, kSiteBadLength);
+    cta_range = cta_last = decode_tiles(own_len);
+    __syncthreads();
+  } else {
+    const long long total = s_pre[kDecodeThreads] * hv_count;
+    cta_range = (total + gridDim.x - 1) / gridDim.x;
+    cta_first = blockIdx.x * cta_range;
+    cta_last = cta_first + cta_range < total ? cta_first + cta_range : total;
+  }
   const long long warp_range = (cta_range + kDecodeWarps - 1) / kDecodeWarps;
   const long long first = cta_first + warp * warp_range;
   const long long last = first + warp_range < cta_last ? first + warp_range : cta_last;
@@ -176,7 +197,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   // ---- where the range begins ----
   DecodeAt at{};
   at.place = last;                        // nothing to do
-  if (first < last) {
+  if (first < last && p.whole) {
+    at = DecodeAt{own_b, static_cast<int>(blockIdx.x) % hv_count, static_cast<int>(first),
+                  static_cast<int>(cta_last), own_len, first};
+  } else if (first < last) {
     int lo = 0, hi = kDecodeThreads;      // the last run that begins at or before the range
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -411,8 +435,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   __syncthreads();
 
   // ---- join the CTA's pieces, segment by segment ----
-  if (threadIdx.x == 0) p.tail[blockIdx.x].valid = 0;
-  for (int i = 0; i < 2 * kDecodeWarps;) {
+  // (one or two segments: by all threads; more of them, of few pieces each: by a warp each)
+  int segments = 0;
+  long long seen = -1;
+  for (int i = 0; i < 2 * kDecodeWarps; ++i)
+    if (s_piece[i].kind != 0 && s_piece[i].begin != seen) {
+      seen = s_piece[i].begin;
+      ++segments;
+    }
+  const bool by_warp = segments > 2;
+  const int rank = by_warp ? lane : threadIdx.x;
+  for (int i = 0, g = 0; i < 2 * kDecodeWarps;) {
     if (s_piece[i].kind == 0) {
       ++i;
       continue;
@@ -421,45 +454,74 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     const int b = s_piece[i].b, hv = s_piece[i].hv, tiles = s_piece[i].tiles;
     int j = i + 1;
     while (j < 2 * kDecodeWarps && (s_piece[j].kind == 0 || s_piece[j].begin == begin)) ++j;
+    if (by_warp && g++ % kDecodeWarps != warp) {
+      i = j;
+      continue;
+    }
     int h0;
     const int rows = decode_heads(p, hv, h0);
     const bool starts = begin >= cta_first, ends = begin + tiles <= cta_last;
-    for (int u = threadIdx.x; u < rows * (D / 4); u += kDecodeThreads) {
-      const int row = u / (D / 4), col = 4 * (u % (D / 4));
-      float mt = -INFINITY, lt = 0.f;
-      for (int k = i; k < j; ++k)
-        if (s_piece[k].kind) mt = fmaxf(mt, s_ml[k][row].x);
-      const float mu = mt == -INFINITY ? 0.f : mt;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    // kTeam threads, 4 columns of a row at a time, all of a thread's places of a piece loaded at once
+    auto join = [&](auto team) {
+      constexpr int kTeam = decltype(team)::value;
+      constexpr int kPlaces = (ROWS * (D / 4) + kTeam - 1) / kTeam;
+      float4 sum[kPlaces];
+      float mt[kPlaces], lt[kPlaces];
+#pragma unroll
+      for (int x = 0; x < kPlaces; ++x) {
+        const int row = min((rank + kTeam * x) / (D / 4), rows - 1);
+        mt[x] = -INFINITY;
+        lt[x] = 0.f;
+        sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = i; k < j; ++k)
+          if (s_piece[k].kind) mt[x] = fmaxf(mt[x], s_ml[k][row].x);
+      }
       for (int k = i; k < j; ++k) {
         const int kind = s_piece[k].kind;
         if (kind == 0) continue;
         const float* src = kind == 1
             ? p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + k / 2) * p.rows * D
             : reinterpret_cast<const float*>(smem + (k / 2) * (L::kStages * L::kStage));
-        const float4 x = *reinterpret_cast<const float4*>(src + row * D + col);
-        const float w = fast_exp2(s_ml[k][row].x - mu);
-        lt = fmaf(s_ml[k][row].y, w, lt);
-        sum.x = fmaf(x.x, w, sum.x);
-        sum.y = fmaf(x.y, w, sum.y);
-        sum.z = fmaf(x.z, w, sum.z);
-        sum.w = fmaf(x.w, w, sum.w);
+        float4 v[kPlaces];
+#pragma unroll
+        for (int x = 0; x < kPlaces; ++x) {
+          const int u = rank + kTeam * x, row = min(u / (D / 4), rows - 1);
+          v[x] = *reinterpret_cast<const float4*>(src + row * D + 4 * (u % (D / 4)));
+        }
+#pragma unroll
+        for (int x = 0; x < kPlaces; ++x) {
+          const int row = min((rank + kTeam * x) / (D / 4), rows - 1);
+          const float2 ml = s_ml[k][row];
+          const float w = fast_exp2(ml.x - (mt[x] == -INFINITY ? 0.f : mt[x]));
+          lt[x] = fmaf(ml.y, w, lt[x]);
+          sum[x].x = fmaf(v[x].x, w, sum[x].x);
+          sum[x].y = fmaf(v[x].y, w, sum[x].y);
+          sum[x].z = fmaf(v[x].z, w, sum[x].z);
+          sum[x].w = fmaf(v[x].w, w, sum[x].w);
+        }
       }
-      if (starts && ends) {
-        const float inv = 1.f / lt;
-        uint2 w2;
-        w2.x = pack_bf16(sum.x * inv, sum.y * inv);
-        w2.y = pack_bf16(sum.z * inv, sum.w * inv);
-        *reinterpret_cast<uint2*>(p.o + b * p.o_sb + static_cast<long long>(h0 + row) * D + col) = w2;
-        if (p.lse && col == 0)
-          p.lse[static_cast<long long>(b) * p.Hq + h0 + row] = (mt + log2f(lt)) * 0.6931471805599453f;
-      } else {
-        const long long part = (blockIdx.x * 2ll + (starts ? 1 : 0)) * p.rows + row;
-        *reinterpret_cast<float4*>(p.part_o + part * D + col) = sum;
-        if (col == 0) p.part_ml[part] = make_float2(mt, lt);
+#pragma unroll
+      for (int x = 0; x < kPlaces; ++x) {
+        const int u = rank + kTeam * x, row = u / (D / 4), col = 4 * (u % (D / 4));
+        if (row >= rows) continue;
+        if (starts && ends) {
+          const float inv = 1.f / lt[x];
+          uint2 w2;
+          w2.x = pack_bf16(sum[x].x * inv, sum[x].y * inv);
+          w2.y = pack_bf16(sum[x].z * inv, sum[x].w * inv);
+          *reinterpret_cast<uint2*>(p.o + b * p.o_sb + static_cast<long long>(h0 + row) * D + col) = w2;
+          if (p.lse && col == 0)
+            p.lse[static_cast<long long>(b) * p.Hq + h0 + row] = (mt[x] + log2f(lt[x])) * 0.6931471805599453f;
+        } else {
+          const long long part = (blockIdx.x * 2ll + (starts ? 1 : 0)) * p.rows + row;
+          *reinterpret_cast<float4*>(p.part_o + part * D + col) = sum[x];
+          if (col == 0) p.part_ml[part] = make_float2(mt[x], lt[x]);
+        }
       }
-    }
-    if (starts && !ends && threadIdx.x == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
+    };
+    if (by_warp) join(IntConst<32>{});
+    else join(IntConst<kDecodeThreads>{});
+    if (starts && !ends && rank == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
     i = j;
   }
 }
@@ -484,36 +546,25 @@ __global__ void __launch_bounds__(kDecodeJoinThreads) s2_decode_join_kernel(cons
   const int n = static_cast<int>((t.begin + t.tiles - 1) / t.cta_range) - cta + 1;
   auto part = [&](int i) { return ((cta + i) * 2ll + (i == 0 ? 1 : 0)) * p.rows + row; };
   float m = -INFINITY, l = 0.f, acc[kPer] = {};
-  for (int base = warp; base < n; base += 32 * kWarps) {
-    const int i = base + kWarps * lane, cnt = min(32, (n - base + kWarps - 1) / kWarps);
-    const float2 ml = i < n ? p.part_ml[part(i)] : make_float2(-INFINITY, 0.f);
-    float mx = ml.x;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const float2 ml = p.part_ml[part(i)];
+    const float* src = p.part_o + part(i) * D + lane * kPer;
+    float v[kPer];
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      v[0] = x.x; v[1] = x.y;
+    }
+    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
     const float alpha = fast_exp2(m - mu), w = fast_exp2(ml.x - mu);
-    l = l * alpha + ml.y * w;             // this lane's partials
+    l = l * alpha + ml.y * w;
     m = mn;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= alpha;
-#pragma unroll 8
-    for (int k = 0; k < cnt; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* src = p.part_o + part(base + kWarps * k) * D + lane * kPer;
-      float v[kPer];
-      if constexpr (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x; v[1] = x.y;
-      }
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(v[e], wk, acc[e]);
-    }
+    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * alpha + v[e] * w;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
   for (int e = 0; e < kPer; ++e) s_o[warp][lane * kPer + e] = acc[e];
   if (lane == 0) s_ml[warp] = make_float2(m, l);

@@ -157,7 +157,7 @@ s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t st
     s2::s2_decode_kernel<D, 16><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "s2_decode_kernel launch");
-  if (grid == 1) return S2ATTN_OK;   // nothing crosses CTAs
+  if (grid == 1 || p.whole) return S2ATTN_OK;   // nothing crosses CTAs
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -356,7 +356,10 @@ s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_ca
   const long long tiles = static_cast<long long>(B) * Hkv * p.chunks *
                           ((static_cast<long long>(max_pages) * page_size - 1) / s2::kDecodeTile + 1 +
                            s2::kDecodeGap);
-  const int grid = static_cast<int>(std::min<long long>(std::min(num_sms, s2::kDecodeMaxCtas), tiles));
+  const long long segments = static_cast<long long>(B) * Hkv * p.chunks;
+  const int most = std::min(num_sms, s2::kDecodeMaxCtas);
+  p.whole = segments <= most && max_pages * page_size <= s2::kDecodeWholeTokens;
+  const int grid = static_cast<int>(p.whole ? segments : std::min<long long>(most, tiles));
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_decode<64>(p, grid, sm) : launch_decode<128>(p, grid, sm);
 }

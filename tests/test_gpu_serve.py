@@ -240,6 +240,9 @@ DECODE = [
     ([5000, 20000], 8, 8, 128, 64, "apart"),       # segments across warps and CTAs, one row each
     ([12000], 24, 2, 64, 16, "apart"),             # 12 rows: partials of 16-row warps
     ([47] * 40 + [4000], 8, 1, 128, 16, "apart"),
+    ([500, 0, 77, 511, 16], 40, 2, 64, 32, "apart"),   # whole segments: 512 tokens at most, chunks of a group
+    ([300] * 37, 4, 4, 128, 100, "kv_by_page"),    # ... one for each of 148 CTAs
+    ([300] * 38, 4, 4, 128, 100, "kv_by_page"),    # ... and one sequence too many for that
 ]
 
 
