@@ -12,17 +12,20 @@
 // Memory bound: every element is read once and written once or twice. A block takes kTok tokens;
 // one lane per token finds its sequence (binary search of cu_seqlens) and slot, and all threads the
 // tokens' angles, shared by all heads through shared memory. The work then is units of one 16-byte
-// chunk of a head's first half and its partner D/2 columns on, for 8 tokens: 16 loads of 16 bytes in
-// flight a thread, the first ones issued before the slots and angles are known. 8 tokens a block
-// where the heads give a block's threads work, 32 where they do not (fewer than half a block's
+// chunk of a head's first half and its partner D/2 columns on, for 4 tokens: 8 loads of 16 bytes in
+// flight a thread, 128 KB an SM, the first ones issued before the slots and angles are known. 4 tokens a
+// block where the heads give a block's threads work, 32 where they do not (fewer than half a block's
 // threads). A grid of few blocks splits the heads over its second axis.
+// Measured (device time): 32768 tokens of 64 + 2 x 8 heads, d = 128: 217 us, 6.5 TB/s (8-token units and
+// blocks: 218 us, and 4.8 against 3.8 us for a batch of 64 tokens); 9830 tokens of 4 + 2 x 4 heads, d = 64:
+// 12.5 us, 2.8 TB/s, bound by the chain of lookups of a single wave of blocks.
 #pragma once
 
 #include "s2_serve_common.cuh"
 
 namespace s2 {
 
-constexpr int kAppendUnit = 8;            // tokens of a work unit
+constexpr int kAppendUnit = 4;            // tokens of a work unit
 constexpr int kAppendThreads = 256;
 
 struct AppendParams {
@@ -47,7 +50,7 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
 }
 
 template <int D, int kTok>
-__global__ void __launch_bounds__(kAppendThreads) s2_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kHalf = D / 2;
   constexpr int kChunks = D / 16;        // work items of a head: a 16-byte chunk and its partner
   constexpr int kSubs = kTok / kAppendUnit;
