@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library (libs2attn.so) in-tree with nvcc.
+"""Build the sm_100a shared library (libs2attn.so) in-tree with nvcc, and the torch binding of the serving
+entries (_s2torch.so, host code only) with the host compiler.
 
 Usage: python -m shifted_sparse_attention_fwd_b200.build [--verbose]
 """
@@ -8,11 +9,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRCS = [os.path.join(PKG_DIR, "csrc", f) for f in ("s2attn_api.cu", "s2serve_api.cu")]
 LIB = os.path.join(PKG_DIR, "libs2attn.so")
+BINDING_SRC = os.path.join(PKG_DIR, "csrc", "s2_torch.cpp")
+BINDING = os.path.join(PKG_DIR, "_s2torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -36,22 +40,45 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-def build(verbose: bool = False, force: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-t", "0",   # the translation units side by side
-           "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *SRCS]
+def _compile(cmd, out, verbose):
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose:
         print(res.stdout + res.stderr)
-    os.replace(LIB + ".tmp", LIB)
+    os.replace(out + ".tmp", out)
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(ROOT, "include", "s2attn.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    _compile([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+              "-I", sysconfig.get_paths()["include"], "-I", inc,
+              "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, BINDING_SRC,
+              "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+              "-ltorch_python", "-o", BINDING + ".tmp"], BINDING, verbose)
+    return BINDING
+
+
+def build(verbose: bool = False, force: bool = False) -> str:
+    """libs2attn.so and the torch binding; returns the library's path."""
+    if force or not up_to_date():
+        cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+               "-t", "0",   # the translation units side by side
+               "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *SRCS]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        _compile(cmd, LIB, verbose)
+    build_binding(verbose, force)
     return LIB
 
 

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <exception>
 #include <mutex>
 #include <vector>
 
@@ -403,8 +404,12 @@ s2attn_status s2attn_prompt_fwd(const void* q, const void* k, const void* v, voi
   int num_sms = 0;
   if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_prompt<64>(p, maps, cu_seqlens, n_seqs, sm)
-                 : launch_prompt<128>(p, maps, cu_seqlens, n_seqs, sm);
+  try {
+    return d == 64 ? launch_prompt<64>(p, maps, cu_seqlens, n_seqs, sm)
+                   : launch_prompt<128>(p, maps, cu_seqlens, n_seqs, sm);
+  } catch (const std::exception&) {   // the sequences' order is host memory
+    return s2host::fail(S2ATTN_ERR_CUDA, "s2attn_prompt_fwd: out of host memory");
+  }
 }
 
 }  // extern "C"

@@ -114,3 +114,14 @@ def test_binding_refuses_cpu_tensors_types_and_shapes():
         s2.decode(q.float(), kc, kc.clone(), table, lens)
     with pytest.raises(ValueError, match="go together"):
         s2.s2attn_rope_append(q, None, k, None, k, kc, kc, table, lens)
+
+
+def test_binding_is_loud_when_missing_or_of_another_torch(lib, monkeypatch, tmp_path):
+    from shifted_sparse_attention_fwd_b200 import _serve
+    monkeypatch.setattr(_serve, "BINDING_PATH", str(tmp_path / "none.so"))
+    with pytest.raises(RuntimeError, match="build it"):
+        _serve._load()
+    monkeypatch.undo()
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="build it again"):
+        _serve._load()
