@@ -461,3 +461,148 @@ def test_prompt_append_decode_agree():
     _near_bf16(o1, want[last], slack[last])
     assert float((lse.double() - want_lse).abs().max()) <= 2e-5
     assert float((lse1.double() - want_lse[:, last].T).abs().max()) <= 2e-5
+
+
+# ------------------------------------------------------------------------------------------
+# large offsets, graphs, streams, shared pages
+# ------------------------------------------------------------------------------------------
+def test_offsets_past_32_bits():
+    """Pages, rows and heads whose element offsets pass 2^31 and 2^32: caches of 33,000 pages of 64 x 8 x
+    128, K and V interleaved by page, and packed rows 2^17 elements apart."""
+    page, hkv, hq, d = 64, 8, 16, 128
+    pages = 33000
+    both = torch.empty(pages, 2, page, hkv, d, dtype=torch.bfloat16, device="cuda")   # 8.6 GB
+    kc, vc = both[:, 0], both[:, 1]
+    lens = [100, 64, 129]
+    rows = [[32999, 16400, 1 << 30], [16383, 1 << 30, 1 << 30], [0, 32998, 16384]]
+    cu = _cu(lens)
+    T = cu[-1]
+    q, k, v = (_randn(90 + i, T, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    q_rot, k_rot = s2.rope_append(q, k, v, kc, vc, _ints(rows), _ints(lens), _ints(cu))
+    for s, n in enumerate(lens):
+        for t in range(n):
+            pg = rows[s][t // page]
+            assert torch.equal(kc[pg, t % page], k_rot[cu[s] + t]) and torch.equal(vc[pg, t % page], v[cu[s] + t])
+    last = torch.tensor(cu[1:], device="cuda") - 1
+    o, lse = s2.decode(q_rot[last], kc, vc, _ints(rows), _ints(lens))
+    _ok()
+    want, want_lse, mean_abs = _prompt64(q_rot, k_rot, v, cu, d ** -0.5)
+    _near_bf16(o, want[last], (BF16_STEP + 1e-5) * mean_abs[last])
+    assert float((lse.double() - want_lse[:, last].T).abs().max()) <= 2e-5
+    del both, kc, vc
+    # packed rows far apart: row 20,000 of o, q is past 2^31 elements
+    n, before = 300, 20000
+    buf = torch.empty(before + n, 1 << 17, dtype=torch.bfloat16, device="cuda")   # 5.3 GB
+    views = [buf[:, i * 4096:i * 4096 + h * d].unflatten(1, (h, d)) for i, h in enumerate((hq, hkv, hkv, hq))]
+    for i, h in enumerate((hq, hkv, hkv)):
+        views[i][before:] = _randn(95 + i, n, h, d)
+    qv, kv, vv, ov = views
+    lse = torch.empty(hq, before + n, device="cuda")
+    s2.s2attn_prompt_fwd(qv, kv, vv, ov, lse, [before, before + n])
+    _ok()
+    want, want_lse, mean_abs = _prompt64(qv[before:], kv[before:], vv[before:], [0, n], d ** -0.5)
+    _near_bf16(ov[before:], want, (BF16_STEP + 1e-5) * mean_abs)
+    assert float((lse[:, before:].double() - want_lse).abs().max()) <= 2e-5
+
+
+def test_captured_step_of_append_and_decode():
+    """One decoding step captured through the allocating calls, replayed as the sequences grow; the second
+    graph shares nothing with the first and both stay right when replayed in turn."""
+    hq, hkv, d, page, B, pi = 8, 4, 64, 8, 3, 0.5
+    width = 80                                       # 640 tokens: the list form, two launches
+    order = list(range(B * width))
+    random.Random(3).shuffle(order)
+    rows = [order[b * width:(b + 1) * width] for b in range(B)]
+    table = _ints(rows)
+    graphs = []
+    for g in range(2):
+        kc, vc = _randn(5 + g, B * width, page, hkv, d), _randn(7 + g, B * width, page, hkv, d)
+        st = dict(kc=kc, vc=vc, q=_randn(1, B, hq, d), k=_randn(2, B, hkv, d), v=_randn(3, B, hkv, d),
+                  lens=_ints([3, 0, 40]), graph=torch.cuda.CUDAGraph())
+        s2.rope_append(st["q"], st["k"], st["v"], kc.clone(), vc.clone(), table, st["lens"], pi_scale=pi)
+        s2.decode(st["q"], kc, vc, table, st["lens"])
+        torch.cuda.synchronize()
+        with torch.cuda.graph(st["graph"]):
+            st["q_rot"], st["k_rot"] = s2.rope_append(st["q"], st["k"], st["v"], kc, vc, table, st["lens"], pi_scale=pi)
+            st["o"], st["lse"] = s2.decode(st["q_rot"], kc, vc, table, st["lens"])
+        graphs.append(st)
+    lens = [[200, 0, 40], [639, 1, 7]]
+    for step in range(3):
+        for g, st in enumerate(graphs):
+            now = [n + 1 if n else 0 for n in lens[g]]
+            lens[g] = [min(n, 640) for n in now]
+            for x, h in (("q", hq), ("k", hkv), ("v", hkv)):
+                st[x].copy_(_randn(100 + 10 * step + g, B, h, d))
+            st["lens"].copy_(_ints(lens[g]))
+            st["graph"].replay()
+            _ok()
+            for b, n in enumerate(lens[g]):
+                if n:
+                    want = _turn64(st["k"][b:b + 1], torch.tensor([n - 1], device="cuda"), 10000.0, pi)[0]
+                    _near_bf16(st["kc"][rows[b][(n - 1) // page], (n - 1) % page], want, 1.2e-5)
+            _check_decode(st["q_rot"], st["kc"], st["vc"], rows, lens[g], d ** -0.5, st["o"], st["lse"])
+
+
+def test_captured_prompt_and_calls_on_a_side_stream():
+    hq, hkv, d = 6, 3, 64
+    cu = _cu([200, 1, 300])
+    q, k, v = (_randn(i, cu[-1], h, d) for i, h in enumerate((hq, hkv, hkv)))
+    o, lse = s2.prompt_fwd(q, k, v, cu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o1, lse1 = s2.prompt_fwd(q, k, v, cu, stream=side)
+    o2, lse2 = s2.prompt_fwd(q, k, v, cu, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, lse3 = s2.prompt_fwd(q, k, v, cu)
+    graph.replay()
+    _ok()
+    for x, y in ((o1, lse1), (o2, lse2), (o3, lse3)):
+        assert torch.equal(x, o) and torch.equal(y, lse)
+    q.copy_(_randn(9, cu[-1], hq, d))
+    graph.replay()
+    o4, lse4 = s2.prompt_fwd(q, k, v, cu)
+    _ok()
+    assert torch.equal(o3, o4) and torch.equal(lse3, lse4)
+
+
+def test_two_calls_at_once_and_shared_pages():
+    """Decoding steps on two streams at once, and sequences that share the pages of a common prefix."""
+    hq, hkv, d, page = 16, 4, 128, 16
+    prefix = list(range(40))                         # 640 tokens that all sequences share
+    lens = [640 + n for n in (1, 17, 300, 0)]
+    own = [[40], [41, 42], list(range(43, 62)), []]
+    rows = [prefix + x + [1 << 30] * (19 - len(x)) for x in own]
+    kc, vc = _randn(2, 62, page, hkv, d), _randn(3, 62, page, hkv, d)
+    qs = [_randn(10 + i, 4, hq, d) for i in range(2)]
+    want = [s2.decode(q, kc, vc, _ints(rows), _ints(lens)) for q in qs]
+    for q, (o, lse) in zip(qs, want):
+        _check_decode(q, kc, vc, rows, lens, d ** -0.5, o, lse)
+    streams = [torch.cuda.Stream() for _ in qs]
+    table, n = _ints(rows), _ints(lens)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for q, s in zip(qs, streams):
+            with torch.cuda.stream(s):
+                got.append(s2.decode(q, kc, vc, table, n))
+    _ok()
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
+def test_append_without_queries_and_views_of_length_one():
+    hkv, d, page = 1, 64, 1
+    kc, vc = _randn(1, 3, page, hkv, d), _randn(2, 3, page, hkv, d)
+    big = _randn(3, 4, 5, d)
+    k, v = big[1:2, 2:3], big[2:3, 4:5]              # one row, one head: strides of the packed rows
+    q_rot, k_rot = s2.rope_append(None, k, v, kc, vc, _ints([[0, 2]]), _ints([2]))
+    _ok()
+    assert q_rot is None
+    _near_bf16(k_rot, _turn64(k, torch.tensor([1], device="cuda"), 10000.0, 1.0), 1.2e-5)
+    assert torch.equal(kc[2, 0], k_rot[0]) and torch.equal(vc[2, 0], v[0])
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.decode(k, kc[:, :, :, :], vc, _ints([[0, 2]]), _ints([2]), scale=0.0)
+    with pytest.raises(ValueError, match="contiguous"):
+        s2.decode(big.transpose(1, 2)[:, :, :].reshape(4, 5, d).transpose(0, 1)[:, :, ::2], kc, vc, _ints([[0]] * 5), _ints([1] * 5))
