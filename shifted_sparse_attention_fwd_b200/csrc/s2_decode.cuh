@@ -15,7 +15,7 @@
 // inside the CTA, through shared memory; of the segments that cross CTAs, at most two a CTA, the
 // partial results go to the workspace, and a second small kernel, one block per CTA boundary and
 // query row, joins them. Pieces are always added in the list's order, with no atomics: the same
-// bits every time. The second kernel is launched programmatically early and waits on the device.
+// bits every time.
 // Where the block table holds few tokens a sequence and there are no more segments than SMs, each CTA
 // takes a whole segment instead and the second kernel falls away.
 //
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   __shared__ float2 s_ml[2 * kDecodeWarps][ROWS];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_launch_dependents();
+  pdl_wait();
   if (threadIdx.x < 2 * kDecodeWarps) s_piece[threadIdx.x].kind = 0;
   if (threadIdx.x == 0) p.tail[blockIdx.x].valid = 0;
 
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(kDecodeJoinThreads) s2_decode_join_kernel(cons
   __shared__ float2 s_ml[kWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x, row = blockIdx.y;
+  pdl_launch_dependents();
   pdl_wait();
   const DecodeTail t = p.tail[cta];
   if (!t.valid) return;

@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(352, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();                             // (after the set-up, which touches no memory of the caller's)
   const uint32_t tmem = *tmem_slot;
 
   // The k-th unit of this CTA, for a whole warp or one thread.

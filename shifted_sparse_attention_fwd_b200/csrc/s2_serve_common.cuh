@@ -26,8 +26,10 @@ __device__ __forceinline__ void report_bad_index(unsigned int* err, uint32_t ker
   atomicCAS(err, 0u, (kernel << 8) | site);
 }
 
-// Programmatic dependent launch: let the next kernel of the stream start its prologue / wait for
-// the previous kernel's results (its whole grid's memory operations).
+// Programmatic dependent launch. The serving kernels are launched so that they may start before the
+// kernel in front of them in the stream has ended: they wait for it (its whole grid, with its memory
+// operations) before they touch any memory of the caller's, and let the kernel behind them, if it is
+// launched the same way, start as early. A step's kernels take 3 to 6 us each, of which a launch is 1.
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <exception>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 // s2_device.cuh defines this one function out of line; the library's other translation unit has
@@ -60,6 +61,24 @@ s2attn_status serve_device(unsigned int** err, int* num_sms) {
     if (d.err == cudaSuccess) d.err = serve_smem_attrs<128>();
   });
   return d.err == cudaSuccess ? S2ATTN_OK : cuda_fail(d.err, "device set-up");
+}
+
+// A launch that may start before the kernel in front of it has ended (the kernel waits: pdl_wait).
+template <class... Params, class... Args>
+s2attn_status launch_early(const char* what, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, what);
 }
 
 s2attn_status check_heads(int Hq, int Hkv, int d) {
@@ -125,17 +144,16 @@ const unsigned long long* turns(float base, float pi_scale, int d) {
 // 32 tokens a block where one token's heads would leave more than half of a block idle and the
 // tokens still fill the GPU; the heads split over the second axis until two blocks per SM exist.
 template <int D>
-void launch_append(const s2::AppendParams& p, int num_sms, cudaStream_t stream) {
+s2attn_status launch_append(const s2::AppendParams& p, int num_sms, cudaStream_t stream) {
   const int items = (p.Hq + 2 * p.Hkv) * (D / 16);
   const bool wide = items <= s2::kAppendThreads / 2 && p.T >= 32 * num_sms;
   const int tok = wide ? 32 : s2::kAppendUnit;
   const int groups = (p.T - 1) / tok + 1;
   const int most = (items * (tok / s2::kAppendUnit) + s2::kAppendThreads - 1) / s2::kAppendThreads;
   const dim3 grid(groups, std::max(1, std::min(most, 2 * num_sms / groups)));
-  if (wide)
-    s2::s2_append_kernel<D, 32><<<grid, s2::kAppendThreads, 0, stream>>>(p);
-  else
-    s2::s2_append_kernel<D, s2::kAppendUnit><<<grid, s2::kAppendThreads, 0, stream>>>(p);
+  return launch_early("s2_append_kernel launch",
+                      wide ? s2::s2_append_kernel<D, 32> : s2::s2_append_kernel<D, s2::kAppendUnit>, grid,
+                      s2::kAppendThreads, 0, stream, p);
 }
 
 constexpr size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -152,24 +170,12 @@ DecodeSpace decode_space(int group, int d) {
 
 template <int D>
 s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t stream) {
-  if (p.rows <= 8)
-    s2::s2_decode_kernel<D, 8><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
-  else
-    s2::s2_decode_kernel<D, 16><<<grid, s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "s2_decode_kernel launch");
-  if (grid == 1 || p.whole) return S2ATTN_OK;   // nothing crosses CTAs
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid - 1, p.rows);
-  cfg.blockDim = dim3(s2::kDecodeJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, s2::s2_decode_join_kernel<D>, p);
-  return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_decode_join_kernel launch");
+  const s2attn_status s = launch_early(
+      "s2_decode_kernel launch", p.rows <= 8 ? s2::s2_decode_kernel<D, 8> : s2::s2_decode_kernel<D, 16>, dim3(grid),
+      s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream, p);
+  if (s != S2ATTN_OK || grid == 1 || p.whole) return s;   // one CTA, or whole segments: nothing crosses CTAs
+  return launch_early("s2_decode_join_kernel launch", s2::s2_decode_join_kernel<D>, dim3(grid - 1, p.rows),
+                      s2::kDecodeJoinThreads, 0, stream, p);
 }
 
 // Tensor map over the rows of a packed bf16 [T, H, d] tensor: dims (d, H, T, 1), box (64, 1, rows, 1),
@@ -205,15 +211,12 @@ s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[5], c
                    [&](int a, int b) { return cu[a + 1] - cu[a] > cu[b + 1] - cu[b]; });
   auto launch = [&]() -> s2attn_status {
     const unsigned grid = static_cast<unsigned>(p.Hkv) * per_kv * p.n_tiles;
-    if (heads)
-      s2::s2_prompt_kernel<D, true><<<grid, s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes,
-                                      stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p, work);
-    else
-      s2::s2_prompt_kernel<D, false><<<grid, s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes,
-                                       stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p, work);
+    const s2attn_status s = launch_early(
+        "s2_prompt_kernel launch", heads ? s2::s2_prompt_kernel<D, true> : s2::s2_prompt_kernel<D, false>, dim3(grid),
+        s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes, stream, maps[0], maps[1], maps[2], maps[3],
+        maps[4], p, work);
     p.n_tiles = 0;
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_prompt_kernel launch");
+    return s;
   };
   for (size_t at = 0; at < order.size(); at += s2::kPromptMaxSeqs) {
     const int count = static_cast<int>(std::min<size_t>(s2::kPromptMaxSeqs, order.size() - at));
@@ -292,12 +295,7 @@ s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void
   int num_sms = 0;
   if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
-  if (d == 64)
-    launch_append<64>(p, num_sms, sm);
-  else
-    launch_append<128>(p, num_sms, sm);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? S2ATTN_OK : cuda_fail(e, "s2_append_kernel launch");
+  return d == 64 ? launch_append<64>(p, num_sms, sm) : launch_append<128>(p, num_sms, sm);
 }
 
 size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
