@@ -116,6 +116,11 @@ __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
 }
 __device__ __forceinline__ int decode_tiles(int len) { return len / kDecodeTile + (len % kDecodeTile != 0); }
 
+// n / d, by a 32-bit division where n fits (a 64-bit one takes hundreds of cycles at the kernel's start).
+__device__ __forceinline__ unsigned long long div_near(unsigned long long n, unsigned int d) {
+  return n >> 32 ? n / d : static_cast<unsigned int>(n) / d;
+}
+
 template <int N>
 struct IntConst {
   static constexpr int value = N;
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     __syncthreads();
   } else {
     const long long total = s_pre[kDecodeThreads] * hv_count;
-    cta_range = (total + gridDim.x - 1) / gridDim.x;
+    cta_range = static_cast<long long>(div_near(total + gridDim.x - 1, gridDim.x));
     cta_first = blockIdx.x * cta_range;
     cta_last = cta_first + cta_range < total ? cta_first + cta_range : total;
   }
@@ -202,11 +207,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     at = DecodeAt{own_b, static_cast<int>(blockIdx.x) % hv_count, static_cast<int>(first),
                   static_cast<int>(cta_last), own_len, first};
   } else if (first < last) {
-    int lo = 0, hi = kDecodeThreads;      // the last run that begins at or before the range
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s_pre[mid] * hv_count <= first) lo = mid; else hi = mid;
-    }
+    // the last run that begins at or before the range: eight runs a lane
+    int below = 0;
+#pragma unroll
+    for (int i = 0; i < kDecodeThreads / 32; ++i) below += s_pre[32 * i + lane] * hv_count <= first;
+    const int lo = __reduce_add_sync(0xffffffffu, below) - 1;
     long long begin = s_pre[lo];
     at.b = lo * per;
     for (;;) {
@@ -216,9 +221,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
       begin += places(at.tiles);
       ++at.b;
     }
-    const long long in = first - begin * hv_count;
-    at.hv = static_cast<int>(in / places(at.tiles));
-    at.tile = static_cast<int>(in % places(at.tiles)) - kDecodeGap;
+    const unsigned long long in = first - begin * hv_count;
+    const unsigned int each = places(at.tiles);
+    at.hv = static_cast<int>(div_near(in, each));
+    at.tile = static_cast<int>(in - static_cast<unsigned long long>(at.hv) * each) - kDecodeGap;
     at.place = first;
     if (at.tile < 0) {                    // in the gap before a segment
       at.place -= at.tile;
@@ -437,28 +443,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
 
   // ---- join the CTA's pieces, segment by segment ----
   // (one or two segments: by all threads; more of them, of few pieces each: by a warp each)
-  int segments = 0;
-  long long seen = -1;
-  for (int i = 0; i < 2 * kDecodeWarps; ++i)
-    if (s_piece[i].kind != 0 && s_piece[i].begin != seen) {
-      seen = s_piece[i].begin;
-      ++segments;
-    }
-  const bool by_warp = segments > 2;
+  // Lane x looks at piece x: `live` are the pieces there are, `heads` the first ones of their segments.
+  const bool is_piece = lane < 2 * kDecodeWarps && s_piece[lane & (2 * kDecodeWarps - 1)].kind != 0;
+  const long long my_begin = s_piece[lane & (2 * kDecodeWarps - 1)].begin;
+  const unsigned int live = __ballot_sync(0xffffffffu, is_piece);
+  const unsigned int before = live & ((1u << lane) - 1u);
+  const long long last_begin = __shfl_sync(0xffffffffu, my_begin, before ? 31 - __clz(before) : 0);
+  const unsigned int heads = __ballot_sync(0xffffffffu, is_piece && (before == 0 || last_begin != my_begin));
+  const bool by_warp = __popc(heads) > 2;
   const int rank = by_warp ? lane : threadIdx.x;
-  for (int i = 0, g = 0; i < 2 * kDecodeWarps;) {
-    if (s_piece[i].kind == 0) {
-      ++i;
-      continue;
-    }
+  int g = 0;
+  for (unsigned int todo = heads; todo; todo &= todo - 1, ++g) {
+    if (by_warp && g % kDecodeWarps != warp) continue;
+    const int i = __ffs(todo) - 1;
+    const unsigned int rest = todo & (todo - 1);
+    // the segment's pieces
+    const unsigned int mine = live & ~((1u << i) - 1u) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xffffffffu);
     const long long begin = s_piece[i].begin;
     const int b = s_piece[i].b, hv = s_piece[i].hv, tiles = s_piece[i].tiles;
-    int j = i + 1;
-    while (j < 2 * kDecodeWarps && (s_piece[j].kind == 0 || s_piece[j].begin == begin)) ++j;
-    if (by_warp && g++ % kDecodeWarps != warp) {
-      i = j;
-      continue;
-    }
     int h0;
     const int rows = decode_heads(p, hv, h0);
     const bool starts = begin >= cta_first, ends = begin + tiles <= cta_last;
@@ -474,13 +476,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
         mt[x] = -INFINITY;
         lt[x] = 0.f;
         sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = i; k < j; ++k)
-          if (s_piece[k].kind) mt[x] = fmaxf(mt[x], s_ml[k][row].x);
+        for (unsigned int m = mine; m; m &= m - 1) mt[x] = fmaxf(mt[x], s_ml[__ffs(m) - 1][row].x);
       }
-      for (int k = i; k < j; ++k) {
-        const int kind = s_piece[k].kind;
-        if (kind == 0) continue;
-        const float* src = kind == 1
+      for (unsigned int m = mine; m; m &= m - 1) {
+        const int k = __ffs(m) - 1;
+        const float* src = s_piece[k].kind == 1
             ? p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + k / 2) * p.rows * D
             : reinterpret_cast<const float*>(smem + (k / 2) * (L::kStages * L::kStage));
         float4 v[kPlaces];
@@ -523,7 +523,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     if (by_warp) join(IntConst<32>{});
     else join(IntConst<kDecodeThreads>{});
     if (starts && !ends && rank == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
-    i = j;
   }
 }
 
