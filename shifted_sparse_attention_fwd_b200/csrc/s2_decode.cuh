@@ -20,12 +20,19 @@
 // takes a whole segment instead and the second kernel falls away.
 //
 // A warp is on its own: it copies its tiles' rows to its part of shared memory with 16-byte
-// asynchronous copies (the row's page looked up one tile ahead), kDecodeStages tiles deep, so
-// copies run ahead across segment boundaries, and there is no barrier between warps. Copies of single rows take any page size and any
-// stride. The products run on mma.sync (16 query rows x 8 keys x 16): at 6.5 TB/s the products of
-// 16 padded rows need about 100 TFLOP/s, far below what it reaches, and the fragment of the scores
-// is the fragment of P in the second product, in registers. Scores, maxima, sums and outputs are
-// fp32; P is rounded to bf16 for the tensor cores as in the other attention kernels.
+// asynchronous copies (the row's page looked up one tile ahead), three tiles deep at D = 128 and six
+// at 64, across segment boundaries, and there is no barrier between warps. Copies of single rows take
+// any page size and any stride. The products run on mma.sync (16 query rows x 8 keys x 16): at 6.5
+// TB/s the products of 16 padded rows need about 100 TFLOP/s, far below what it reaches, and the
+// fragment of the scores is the fragment of P in the second product, in registers. Scores, maxima,
+// sums and outputs are fp32; P is rounded to bf16 for the tensor cores, to twice bf16 where the MMA's
+// rows have room (8 query rows and less).
+//
+// Measured: 16 sequences of about 8k tokens, 32 kv heads, 2.0 GB: 314 us, 6.5 TB/s (of measured copy
+// bandwidth: 0.98). One sequence of 102400 tokens, 8 kv heads, 419 MB: 73 us; the stream itself runs at
+// 7.3 TB/s, 2 us pass before the first copy is on its way, 3 before it is there, 4 at the ranges' uneven
+// ends and 5 in the second kernel. 64 sequences of 1 to 32768 tokens, 662 MB: 114 us. Tried: 12 warps two
+// tiles deep and K and V copied in groups of their own (not faster), wider L2 fetches (no change).
 #pragma once
 
 #include "s2_device.cuh"
@@ -37,8 +44,10 @@ constexpr int kDecodeWarps = 8;
 constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kDecodeTile = 16;           // tokens
 constexpr int kDecodeRows = 16;           // query heads a warp takes at a time (one MMA's rows)
+// (1 to 3 places: 114 to 117 us on the ragged batch, 73 to 79 us on the long sequence, 1 best over both)
 constexpr int kDecodeGap = 1;
-// At most this many tokens a sequence, and no more segments than SMs: a CTA takes a whole segment.
+// At most this many tokens a sequence, and no more segments than SMs: a CTA takes a whole segment (one
+// sequence of 131 tokens, 4 heads: 6.3 us of device time instead of 8, and one launch instead of two).
 constexpr int kDecodeWholeTokens = 512;
 constexpr int kDecodeMaxCtas = 148;       // the workspace has room for this many CTAs' partials
 constexpr int kDecodeJoinThreads = 256;
@@ -139,7 +148,7 @@ __device__ __forceinline__ int decode_heads(const DecodeParams& p, int hv, int& 
   return min(kDecodeRows, (kvh + 1) * p.group - h0);
 }
 
-// ROWS: 8 or 16 query rows a warp computes (the MMA has 16; with 8 the upper ones' softmax is left out).
+// ROWS: 8 or 16 query rows a warp computes (the MMA has 16).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __grid_constant__ DecodeParams p) {
   using L = DecodeLayout<D>;
@@ -373,6 +382,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
         for (int j = 0; j < D / 8; ++j) {
           acc[j][2 * half] *= alpha;
           acc[j][2 * half + 1] *= alpha;
+          if (ROWS == 8) {
+            acc[j][2] *= alpha;
+            acc[j][3] *= alpha;
+          }
         }
         m[half] = cand;
       }
@@ -382,7 +395,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
         const float e0 = fast_exp2(fmaf(s[t][2 * half], p.scale_log2, -mu));
         const float e1 = fast_exp2(fmaf(s[t][2 * half + 1], p.scale_log2, -mu));
         l[half] += e0 + e1;
-        pf[2 * t + half] = pack_bf16(e0, e1);
+        const uint32_t hi = pack_bf16(e0, e1);
+        pf[2 * t + half] = hi;
+        // With 8 rows the MMA's other 8 carry what the rounding of P to bf16 leaves, so that the product
+        // has P to 16 bits at no cost (output error 0.0023 -> 0.0017, that of its own rounding).
+        if (ROWS == 8) pf[2 * t + 1] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
       }
     }
 #pragma unroll
@@ -399,6 +416,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     const bool seg_end = now.tile + 1 == now.tiles, end = at.place >= last;
     if (!seg_end && !end) continue;
     fresh = true;
+    if (ROWS == 8) {
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        acc[j][0] += acc[j][2];
+        acc[j][1] += acc[j][3];
+      }
+    }
     const bool whole = seg_end && seg_tile == 0;
     const int piece = 2 * warp + (end ? 1 : 0);
     float* out = p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + warp) * p.rows * D;
