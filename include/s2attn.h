@@ -428,8 +428,7 @@ S2ATTN_API s2attn_status s2attn_decode(const void* q, const void* k_cache, const
  * call only). Row i of a sequence sees its rows 0..i: o = softmax(scale * q k^T) v, lse fp32 [Hq, T]
  * (natural log). Query head h reads kv head h / (Hq / Hkv); q and k must be turned already
  * (s2attn_rope_append with k_rot, s2attn_rope_pi). Rows of no sequence are neither read into a
- * result nor written. A value row that is not finite may turn the rows before it in its own 128 rows of
- * the sequence into NaN as well (0 * NaN); it does not reach other sequences.
+ * result nor written, and what a row does not see never reaches it, NaN and infinities included.
  * `strides`: NULL or the row strides of {q, k, v, o}, multiples of 8 and at least heads * d; tensors
  * must not overlap. T > 2^23 or Hq >= 2^20 -> S2ATTN_ERR_UNSUPPORTED. One launch per 512 sequences and
  * 2048 query tiles (of 128 rows, or 256 where Hq / Hkv is odd); a captured graph keeps the lengths it was

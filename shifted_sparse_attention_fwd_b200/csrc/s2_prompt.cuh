@@ -14,11 +14,12 @@
 // the order of the grid, with no counter in memory. The order is by chunks of kv heads whose K and V
 // fit L2 together, the heaviest query tiles of all sequences first in each chunk.
 //
-// Warp roles (352 threads):
+// Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1: thread i owns row i (TMEM lane i), fp32 online
 //                   softmax, P written to TMEM as bf16 over S, epilogue.
 //   warp 8          producer: next unit, TMA loads (Q tiles, K ring, V ring).
 //   warps 9, 10     MMA issuer of query tile 0 / 1 (one lane): S_t(0), then PV_t(j), S_t(j + 1), ...
+//   warp 11         looks through the value tiles that a query tile sees in part.
 // TMEM columns: S0/P0 [0,128), S1/P1 [128,256), O0 [256,256+D), O1 [256+D, 256+2D).
 //
 // One tile's MMAs run beside the other tile's softmax. Each tile has an issuer of its own, so that neither
@@ -26,21 +27,26 @@
 // run (one issuer for both: 109 cycles per 128 x 128 x 16 MMA even with no softmax at all, against 64).
 //
 // Softmax pass: the exponentials are taken against a reference that need not be the maximum: the maximum
-// of the row's first 32 scores. It only has to keep the sums inside fp32, and products and sums keep their
+// of the row's first 16 scores. It only has to keep the sums inside fp32, and products and sums keep their
 // relative precision at any scale, so no maximum is searched for as long as a tile's row sum stays
 // below 2^30; else the pass is repeated from S, which is still in TMEM, against the maximum so far, and
 // O and l are rescaled.
 //
-// Measured: one prompt of 8192 tokens, 32 heads, d = 128: 0.50 ms alone, 0.56 ms in a loop (1.0 PFLOP/s of
-// visible work); 39k tokens in two prompts, 64 / 8 heads: 1.07 PFLOP/s. Tensor pipe and exponential unit
-// are each 53 % busy at 1.7 GHz: in a loop the GPU sits at its power cap (985 W), and a pass takes 0.55 J, of
-// which the MMAs alone need 0.36 (the same launch with the softmax left out) and cuBLAS 0.39 for as many
-// flops: energy, not a pipe, bounds it. Tried without gain: key tiles of 64 with two score buffers per query
-// tile (N = 64 MMAs: 0.79 ms), a warpgroup of its own for the epilogue (128 registers a thread at launch spill
-// the softmax: 0.79 ms), turns taken by the MMA issuers instead of the softmax (0.59 ms).
+// Measured, in a loop: one prompt of 8192 tokens, 32 heads, d = 128: 0.55 ms, 1.0 PFLOP/s of visible work; 39k
+// tokens in two prompts, 64 / 8 heads: 1.09 PFLOP/s; 12 prompts of 1 to 4999 tokens, 32 heads: 0.263 ms, 0.85.
+// Tensor pipe and exponential unit are each a good half busy at 1.7 GHz: the GPU sits at its power cap (990 W),
+// and a pass over the 8192 tokens takes 0.54 J, of which the MMAs alone need 0.36 (the same launch with the
+// softmax left out) and cuBLAS 0.39 for as many flops: energy, not a pipe, bounds it. Scores are loaded 16
+// columns at a time so that nothing spills (164 registers; 32 at a time: 4 % slower). Tried without gain: key
+// tiles of 64 with two score buffers per query tile (N = 64 MMAs: 0.79 ms), a warpgroup of its own for the
+// epilogue (128 registers a thread at launch spill the softmax: 0.79 ms), turns taken by the MMA issuers
+// instead of the softmax (0.59 ms).
 //
-// Rows of other sequences in a tile: their keys are masked; their values, whatever they hold
-// (0 * NaN), never reach a product: the last V tile of a sequence is loaded without them.
+// Masked places hold anything. Keys are masked by selection. Values would reach a product as 0 * NaN: rows
+// of other sequences are not loaded (the last V tile of a sequence is filled up with zeros), and warp 11
+// looks through the diagonal V tiles, which hold rows that some query rows do not see: infinities and NaN
+// are replaced by zeros there, and in such a unit, a rare one, the warp adds them to the stored rows that
+// do see them. (8192 tokens: no time; it has a step's time to look at 32 KB.)
 #pragma once
 
 #include "s2_common.cuh"
@@ -94,16 +100,19 @@ struct PromptLayout {
   static constexpr uint32_t kStage = kV + kStages * kTile;
   static constexpr uint32_t kClc = kStage + 8 * kStageWarp; // response of the launch control, 16 bytes
   static constexpr uint32_t kRing = kClc + 16;
+  static constexpr uint32_t kBad = kRing + kUnitRing * sizeof(PromptUnit);   // units' diagonal tiles
   enum { B_Q = 0, B_QE = 2, B_K = 4, B_KE = B_K + kStages, B_V = B_KE + kStages, B_VE = B_V + kStages,
          B_S = B_VE + kStages, B_P = B_S + 2, B_ODONE = B_P + 2, B_UF = B_ODONE + 2,
-         B_UE = B_UF + kUnitRing, B_CLC = B_UE + kUnitRing, B_DRAIN, B_TURN = B_DRAIN + 2, B_COUNT = B_TURN + 2 };
-  static constexpr uint32_t kBar = (kRing + kUnitRing * sizeof(PromptUnit) + 7) / 8 * 8;
+         B_UE = B_UF + kUnitRing, B_CLC = B_UE + kUnitRing, B_DRAIN, B_TURN = B_DRAIN + 2,
+         B_VC = B_TURN + 2, B_BAD = B_VC + kStages,
+         B_FIX = B_BAD + kUnitRing, B_COUNT = B_FIX + 2 };
+  static constexpr uint32_t kBar = (kBad + kUnitRing * 4 + 7) / 8 * 8;
   static constexpr uint32_t kTmemSlot = kBar + B_COUNT * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
   static constexpr uint32_t kBytes = kAbort + 4;
   // (at least 116 KB, so that one CTA is resident per SM: each takes all of TMEM)
   static constexpr uint32_t kLaunchBytes = kBytes + 1024 > 116 * 1024 ? kBytes + 1024 : 116 * 1024;
-  static constexpr int kThreads = 352;
+  static constexpr int kThreads = 384;
   static_assert(kLaunchBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -156,33 +165,63 @@ __device__ __forceinline__ PromptUnit prompt_unit(const PromptParams& p, const P
   return r;
 }
 
+// The not finite halves of a bf16 pair: bits 15 and 31; and the pair with zeros in their place.
+__device__ __forceinline__ uint32_t bf16x2_not_finite(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t bf16x2_finite_part(uint32_t w) {
+  const uint32_t x = bf16x2_not_finite(w);
+  return w & ~((x & 0x80000000u ? 0xffff0000u : 0u) | (x & 0x8000u ? 0xffffu : 0u));
+}
+
+// Adds to a stored row of O (position `pos` of its sequence, query tile t) the infinities and NaN of the value
+// rows it sees in the unit's diagonal tiles that were found to hold some (weights are positive: inf stays inf).
+template <int D>
+__device__ __forceinline__ void prompt_add_not_finite(const PromptParams& p, const PromptUnit& u, int bad, int t, int pos) {
+  __nv_bfloat16* o = p.o + (u.start + pos) * p.o_st + static_cast<long long>(u.h[t]) * D;
+  for (int x = 0; x < 2; ++x) {
+    if (!((bad >> x) & 1) || (x == 1 && u.n[0] == u.n[1]) || u.n[x] > u.n[t]) continue;
+    const int first = (u.n[x] - 1) * kTileRows, last = min(first + kTileRows - 1, pos);
+    for (int r = first; r <= last; ++r) {
+      const __nv_bfloat16* v = p.v + (u.start + r) * p.v_st + static_cast<long long>(u.kvh) * D;
+      for (int c = 0; c < D; c += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + c);
+        if (!bf16x2_not_finite(w)) continue;
+        for (int i = 0; i < 2; ++i) {
+          const float y = __bfloat162float(v[c + i]);
+          if (!isfinite(y)) o[c + i] = __float2bfloat16(__bfloat162float(o[c + i]) + y);
+        }
+      }
+    }
+  }
+}
+
 // Tensor memory loads whose results may be used after tmem_ld_done.
 #define S2_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
                  "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
-      : S2_R8(0), S2_R8(8), S2_R8(16), S2_R8(24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : S2_R8(0), S2_R8(8)
       : "r"(taddr)
       : "memory");
 }
 #undef S2_R8
 #define S2_U8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
                  "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : S2_U8(0), S2_U8(8), S2_U8(16), S2_U8(24)::"memory");
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : S2_U8(0), S2_U8(8)::"memory");
 }
 #undef S2_U8
 
-// 32 scores of a row: P = exp2(c s - m) as bf16 pairs into pk, the sums into acc. Scores behind column
+// 16 scores of a row: P = exp2(c s - m) as bf16 pairs into pk, the sums into acc. Scores behind column
 // `lim` are masked.
 template <bool kMask>
-__device__ __forceinline__ void softmax32(const uint32_t (&r)[32], int lim, uint64_t c2, uint64_t nm2,
+__device__ __forceinline__ void softmax16(const uint32_t (&r)[16], int lim, uint64_t c2, uint64_t nm2,
                                           uint32_t* pk, uint64_t (&acc)[2]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     float s0 = __uint_as_float(r[2 * i]), s1 = __uint_as_float(r[2 * i + 1]);
     if (kMask) {
       s0 = 2 * i > lim ? -INFINITY : s0;
@@ -194,9 +233,23 @@ __device__ __forceinline__ void softmax32(const uint32_t (&r)[32], int lim, uint
     pk[i] = pack_bf16(e0, e1);
   }
 }
+// The pass over a row's 128 scores, 16 at a time, the next 16 on their way; the first ones are in `a`.
+template <bool kMask>
+__device__ __forceinline__ void softmax_row(uint32_t s_col, uint32_t (&a)[16], uint32_t (&b)[16], int lim, uint64_t c2,
+                                            uint64_t nm2, uint32_t (&pk)[64], uint64_t (&acc)[2]) {
+#pragma unroll
+  for (int q = 0; q < 8; q += 2) {
+    tmem_ld16_begin(s_col + 16 * q + 16, b);
+    softmax16<kMask>(a, lim - 16 * q, c2, nm2, pk + 8 * q, acc);
+    tmem_ld_done(b);
+    if (q < 6) tmem_ld16_begin(s_col + 16 * q + 32, a);
+    softmax16<kMask>(b, lim - 16 * q - 16, c2, nm2, pk + 8 * q + 8, acc);
+    if (q < 6) tmem_ld_done(a);
+  }
+}
 
 template <int D, bool kHeads>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     s2_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV8,
                      const __grid_constant__ CUtensorMap tmO8, const __grid_constant__ PromptParams p,
@@ -210,6 +263,7 @@ __global__ void __launch_bounds__(352, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   PromptUnit* ring = reinterpret_cast<PromptUnit*>(smem + L::kRing);
+  volatile int* bad_tiles = reinterpret_cast<volatile int*>(smem + L::kBad);
   const WaitCtx ctx{abort_flag, p.err, p.timeout_ns, KID_PROMPT};
 
   if (warp == 8 && lane == 0) {
@@ -224,15 +278,18 @@ __global__ void __launch_bounds__(352, 1)
       mbar_init(bar(L::B_K + s), 1);
       mbar_init(bar(L::B_KE + s), 2);     // both issuers
       mbar_init(bar(L::B_V + s), 1);
-      mbar_init(bar(L::B_VE + s), 2);
+      mbar_init(bar(L::B_VE + s), 3);     // ... and warp 11
+      mbar_init(bar(L::B_VC + s), 1);
     }
     for (int s = 0; s < kUnitRing; ++s) {
       mbar_init(bar(L::B_UF + s), 1);
-      mbar_init(bar(L::B_UE + s), 10);    // the eight softmax warps and the two issuers
+      mbar_init(bar(L::B_UE + s), 11);    // the eight softmax warps, the two issuers and warp 11
+      mbar_init(bar(L::B_BAD + s), 1);
     }
     mbar_init(bar(L::B_CLC), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L::B_TURN + s), 4);
+      mbar_init(bar(L::B_FIX + s), 4);
       mbar_init(bar(L::B_DRAIN + s), 1);
     }
     *abort_flag = 0;
@@ -382,7 +439,57 @@ __global__ void __launch_bounds__(352, 1)
     for (int i = v_issued - L::kStages; i < v_issued; ++i)
       if (i >= 0) drain_wait(bar(L::B_V + i % L::kStages), (i / L::kStages) & 1, p.timeout_ns);
     if (clc_open) drain_wait(bar(L::B_CLC), clc_asked & 1, p.timeout_ns);
-  } else if (warp >= 9) {
+  } else if (warp == 11) {
+    // ---------------- the diagonal value tiles ----------------
+    int v_seen = 0, fixed[2] = {0, 0};    // V tiles, and units mended, so far
+    bool ok = true;
+    for (int ku = 0; ok; ++ku) {
+      PromptUnit u;
+      if (!read_rec(ku, u, true, 16)) break;
+      int bad = 0;                        // bit t: query tile t's diagonal tile holds infinities or NaN
+      const int n = max(u.n[0], u.n[1]);
+      for (int j = 0; j < n; ++j, ++v_seen) {
+        // (it waits for every tile and releases it too, so that it never falls a phase behind)
+        const int st = v_seen % L::kStages;
+        if (!warp_wait(bar(L::B_V + st), (v_seen / L::kStages) & 1, ctx, 17)) { ok = false; break; }
+        const int diag = (j + 1 == u.n[0] ? 1 : 0) | (j + 1 == u.n[1] ? 2 : 0);
+        if (diag) {
+          uint4* tile = reinterpret_cast<uint4*>(smem + L::kV + st * L::kTile);
+          uint32_t seen = 0;
+#pragma unroll 4
+          for (int x = lane; x < static_cast<int>(L::kTile / 16); x += 32) {
+            const uint4 w = tile[x];
+            seen |= bf16x2_not_finite(w.x) | bf16x2_not_finite(w.y) | bf16x2_not_finite(w.z) | bf16x2_not_finite(w.w);
+          }
+          if (__any_sync(0xffffffffu, seen != 0)) {
+            bad |= diag;
+            for (int x = lane; x < static_cast<int>(L::kTile / 16); x += 32) {
+              const uint4 w = tile[x];
+              tile[x] = make_uint4(bf16x2_finite_part(w.x), bf16x2_finite_part(w.y), bf16x2_finite_part(w.z),
+                                   bf16x2_finite_part(w.w));
+            }
+            fence_async_smem();           // the MMAs read the tile through the async proxy
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::B_VC + st));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_VE + st));
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        bad_tiles[ku % kUnitRing] = bad;
+        mbar_arrive(bar(L::B_BAD + ku % kUnitRing));
+      }
+      __syncwarp();
+      for (int t = 0; bad && t < 2; ++t) {           // the rare unit: once its rows are stored
+        if (u.n[t] == 0) continue;
+        if (!warp_wait(bar(L::B_FIX + t), fixed[t]++ & 1, ctx, 20)) { ok = false; break; }
+        const int first = u.qt[t] * kTileRows, left = min(kTileRows, u.len - first);
+        for (int r = lane; r < left; r += 32) prompt_add_not_finite<D>(p, u, bad, t, first + r);
+      }
+    }
+  } else if (warp == 9 || warp == 10) {
     // ---------------- MMA issuers ----------------
     const int t = warp - 9;
     if (lane == 0) {
@@ -390,6 +497,7 @@ __global__ void __launch_bounds__(352, 1)
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
       const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * D, q_smem = sbase + L::kQ + t * L::kTile;
       int k0 = 0, q_used = 0, p_used = 0;  // K/V tiles before this unit; query and P tiles used
+      int checked[L::kStages] = {};        // tiles of each V slot that warp 11 has looked through
       bool ok = true;
       auto wait_tile = [&](int full0, int i, uint32_t site) {
         return wait_bar(bar(full0 + i % L::kStages), (i / L::kStages) & 1, ctx, site);
@@ -408,18 +516,29 @@ __global__ void __launch_bounds__(352, 1)
           if (j + 1 == mine) mma_commit(bar(L::B_QE + t));   // last S on this query tile
           return true;
         };
+        // V(j) is there, and, if it is a query tile's diagonal one, has been looked through.
+        auto wait_v = [&](int j) -> bool {
+          const int st = (k0 + j) % L::kStages;
+          if (!wait_tile(L::B_V, k0 + j, 10)) return false;
+          if (j + 1 != u.n[0] && j + 1 != u.n[1]) return true;
+          int k = 0;
+#pragma unroll
+          for (int x = 0; x < L::kStages; ++x)
+            if (x == st) k = checked[x]++;
+          return wait_bar(bar(L::B_VC + st), k & 1, ctx, 18);
+        };
         if (mine > 0) ok = wait_bar(bar(L::B_Q + t), q_used++ & 1, ctx, 8) && issue_s(0);
         for (int j = 0; ok && j < n; ++j) {
           const int vi = k0 + j, vst = vi % L::kStages;
           if (j >= mine) {
             // The tile does not see these keys: they are released once they are there (a release ahead
             // of the load would count for the slot's last tile).
-            if (!wait_tile(L::B_K, vi, 7) || !wait_tile(L::B_V, vi, 10)) { ok = false; break; }
+            if (!wait_tile(L::B_K, vi, 7) || !wait_v(j)) { ok = false; break; }
             mbar_arrive(bar(L::B_KE + vst));
             mbar_arrive(bar(L::B_VE + vst));
             continue;
           }
-          if (!wait_tile(L::B_V, vi, 10)) { ok = false; break; }
+          if (!wait_v(j)) { ok = false; break; }
           if (!wait_bar(bar(L::B_P + t), p_used++ & 1, ctx, 9)) { ok = false; break; }
           tc_fence_after();
           gemm_ts_mn<D>(o_tmem, s_tmem, sbase + L::kV + vst * L::kTile, idesc_pv, j > 0);
@@ -442,9 +561,11 @@ __global__ void __launch_bounds__(352, 1)
     int s_cnt = 0, o_cnt = 0, turn = 0;
     bool ok = true;
     for (int ku = 0; ok; ++ku) {
-      PromptUnit u;
-      if (!read_rec(ku, u, true, 11)) break;
-      const int n = u.n[wg], n_all = max(u.n[0], u.n[1]);
+      // Of the unit only its tile counts are held through the passes (registers); the rest is read in the
+      // epilogue, and the ring's slot released after it.
+      const int slot = ku % kUnitRing;
+      if (!warp_wait(bar(L::B_UF + slot), (ku / kUnitRing) & 1, ctx, 11) || !ring[slot].live) break;
+      const int n = ring[slot].n[wg], n_all = max(ring[slot].n[0], ring[slot].n[1]);
       float m_run = -INFINITY, l_run = 0.f;
       // The two tiles' passes take turns (tile 0's pass k, tile 1's pass k, tile 0's k + 1, ...): each then
       // has the exponential units to itself while the other tile's MMAs run. Left alone, both warpgroups
@@ -470,66 +591,46 @@ __global__ void __launch_bounds__(352, 1)
         tc_fence_after();
         uint32_t pk[64];
         uint64_t acc[2] = {0, 0};
-        bool exact;
+        bool need;
         {
-          uint32_t a[32], b[32];
+          uint32_t a[16], b[16];
           const bool diag = j + 1 == n;              // the last tile is the diagonal one
-          tmem_ld32_begin(s_col, a);
+          tmem_ld16_begin(s_col, a);
           tmem_ld_done(a);
-          tmem_ld32_begin(s_col + 32, b);
-          if (j == 0) {                              // a first maximum, of 32 scores
+          if (j == 0) {                              // a first reference, the maximum of 16 scores
             float m0 = -INFINITY, m1 = -INFINITY;
             const int lim = diag ? row : kTileRows;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
               m0 = max3f(m0, i > lim ? -INFINITY : __uint_as_float(a[i]), i + 1 > lim ? -INFINITY : __uint_as_float(a[i + 1]));
               m1 = max3f(m1, i + 2 > lim ? -INFINITY : __uint_as_float(a[i + 2]), i + 3 > lim ? -INFINITY : __uint_as_float(a[i + 3]));
             }
             m_run = fmaxf(m0, m1) * c;
           }
           const uint64_t nm2 = f2_pack(-m_run, -m_run);
-          if (diag) {
-            softmax32<true>(a, row, c2, nm2, pk, acc);
-            tmem_ld_done(b);
-            tmem_ld32_begin(s_col + 64, a);
-            softmax32<true>(b, row - 32, c2, nm2, pk + 16, acc);
-            tmem_ld_done(a);
-            tmem_ld32_begin(s_col + 96, b);
-            softmax32<true>(a, row - 64, c2, nm2, pk + 32, acc);
-            tmem_ld_done(b);
-            softmax32<true>(b, row - 96, c2, nm2, pk + 48, acc);
-          } else {
-            softmax32<false>(a, 0, c2, nm2, pk, acc);
-            tmem_ld_done(b);
-            tmem_ld32_begin(s_col + 64, a);
-            softmax32<false>(b, 0, c2, nm2, pk + 16, acc);
-            tmem_ld_done(a);
-            tmem_ld32_begin(s_col + 96, b);
-            softmax32<false>(a, 0, c2, nm2, pk + 32, acc);
-            tmem_ld_done(b);
-            softmax32<false>(b, 0, c2, nm2, pk + 48, acc);
-          }
+          if (diag) softmax_row<true>(s_col, a, b, row, c2, nm2, pk, acc);
+          else softmax_row<false>(s_col, a, b, 0, c2, nm2, pk, acc);
           // (also where it is infinite or NaN)
           const uint64_t both = f2_add(acc[0], acc[1]);
-          const bool need = !(f2_lo(both) + f2_hi(both) <= kPromptMaxSum);
-          exact = __any_sync(0xffffffffu, need);
+          need = !(f2_lo(both) + f2_hi(both) <= kPromptMaxSum);
         }
-        if (exact) {
+        if (__any_sync(0xffffffffu, need)) {
           const int lim = j + 1 == n ? row : kTileRows;
           float mx = -INFINITY;
+          uint32_t a[16], b[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t a[32];
-            tmem_ld32_begin(s_col + 32 * q, a);
+          for (int q = 0; q < 8; ++q) {
+            tmem_ld16_begin(s_col + 16 * q, a);
             tmem_ld_done(a);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float s0 = 32 * q + i > lim ? -INFINITY : __uint_as_float(a[i]);
-              const float s1 = 32 * q + i + 1 > lim ? -INFINITY : __uint_as_float(a[i + 1]);
+            for (int i = 0; i < 16; i += 2) {
+              const float s0 = 16 * q + i > lim ? -INFINITY : __uint_as_float(a[i]);
+              const float s1 = 16 * q + i + 1 > lim ? -INFINITY : __uint_as_float(a[i + 1]);
               mx = max3f(mx, s0, s1);
             }
           }
-          const float m_cand = fmaxf(m_run, mx * c);
+          // (the warp's other rows keep their reference, and so their bits)
+          const float m_cand = need ? fmaxf(m_run, mx * c) : m_run;
           if (__any_sync(0xffffffffu, m_cand != m_run)) {
             // 0 when m_run = -inf; 1 for a row whose scores are all -inf so far
             const float alpha = m_cand == -INFINITY ? 1.f : fast_exp2(m_run - m_cand);
@@ -549,13 +650,9 @@ __global__ void __launch_bounds__(352, 1)
           const float m_use = m_run == -INFINITY ? 0.f : m_run;
           const uint64_t nm2 = f2_pack(-m_use, -m_use);
           acc[0] = acc[1] = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t a[32];
-            tmem_ld32_begin(s_col + 32 * q, a);
-            tmem_ld_done(a);
-            softmax32<true>(a, lim - 32 * q, c2, nm2, pk + 16 * q, acc);
-          }
+          tmem_ld16_begin(s_col, a);
+          tmem_ld_done(a);
+          softmax_row<true>(s_col, a, b, lim, c2, nm2, pk, acc);
         }
         pass_turn();
         tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(pk));
@@ -567,13 +664,17 @@ __global__ void __launch_bounds__(352, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_P + wg));
       }
-      if (n == 0) continue;
+      if (n == 0) {
+        if (lane == 0) mbar_arrive(bar(L::B_UE + slot));
+        continue;
+      }
       if (!ok || !warp_wait(bar(L::B_ODONE + wg), o_cnt & 1, ctx, 13)) { ok = false; break; }
       ++o_cnt;
       tc_fence_after();
       // Epilogue: O / l in bf16 through this warp's staging area (128-byte-swizzled rows of 64
       // columns): atoms of 8 rows inside the sequence go out as TMA boxes, the rows of the atom that
       // the sequence's end cuts as row stores, and rows behind the end not at all.
+      const PromptUnit u = ring[slot];
       const float inv_l = 1.f / l_run;
       uint8_t* stage = smem + L::kStage + warp * L::kStageWarp;
       const uint32_t stage_s = sbase + L::kStage + warp * L::kStageWarp;
@@ -620,6 +721,18 @@ __global__ void __launch_bounds__(352, 1)
       }
       if (lane < left)
         p.lse[static_cast<long long>(u.h[wg]) * p.T + tok + lane] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+      if (!warp_wait(bar(L::B_BAD + slot), (ku / kUnitRing) & 1, ctx, 19)) { ok = false; break; }
+      if (bad_tiles[slot] != 0) {                    // warp 11 has to see the warp's stored rows
+        if (lane == 0) {
+          bulk_wait_all();
+          asm volatile("fence.proxy.async;" ::: "memory");
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_FIX + wg));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_UE + slot));
       tc_fence_before();                  // O is read: the next PV on it waits for this warp's P
     }
     if (lane == 0) bulk_wait_all();
@@ -627,7 +740,7 @@ __global__ void __launch_bounds__(352, 1)
   }
 
   // ---------------- teardown ----------------
-  if (warp >= 9) {                        // each issuer's MMAs are done (a commit covers its own thread's)
+  if (warp == 9 || warp == 10) {          // each issuer's MMAs are done (a commit covers its own thread's)
     if (lane == 0) {
       mma_commit(bar(L::B_DRAIN + warp - 9));
       drain_wait(bar(L::B_DRAIN + warp - 9), 0, p.timeout_ns);

@@ -441,6 +441,44 @@ def test_prompt_growing_scores_and_other_sequences(hq, hkv, d):
         assert float((lse[:, a:e].double() - want_lse).abs().max()) <= 2e-5 + big * 2 ** -20
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (3, 3, 64), (2, 2, 128)])
+def test_prompt_values_of_hidden_rows(hq, hkv, d):
+    """Keys and values that a row does not see never reach it, whatever they hold: rows before a row of NaN
+    or infinities are what they were, to the bit, rows that see it are as the formula has them."""
+    lens = [700, 130, 64, 257]
+    cu = _cu(lens)
+    q, k, v = (_randn(45 + i, cu[-1], h, d) for i, h in enumerate((hq, hkv, hkv)))
+    want, want_lse = s2.prompt_fwd(q, k, v, cu)
+    # (sequence, row, column, value)
+    bad = [(0, 0, 5, "nan"), (0, 255, 0, "inf"), (0, 256, 0, "-inf"), (0, 640, 9, "-inf"), (0, 699, d - 1, "nan"),
+           (1, 129, 33, "inf"), (2, 13, 7, "inf"), (2, 40, 7, "inf"), (3, 127, 1, "nan"), (3, 128, 2, "inf"), (3, 256, 3, "-inf")]
+    sign = torch.zeros(cu[-1], hkv, d, dtype=torch.float64, device="cuda")   # running sum of what is seen
+    for s_, r, c, x in bad:
+        h = (r + c) % hkv
+        v[cu[s_] + r, h, c] = float(x)
+        sign[cu[s_] + r:cu[s_ + 1], h, c] += float(x)
+    o, lse = s2.prompt_fwd(q, k, v, cu)
+    _ok()
+    assert torch.equal(lse, want_lse)
+    seen = sign.repeat_interleave(hq // hkv, 1)
+    clean = seen == 0
+    # a unit that holds such a value has zeros in its place, so nothing else may move
+    assert torch.equal(o[clean], want[clean])
+    got = o.double()
+    assert torch.equal(got[seen.isinf()], seen[seen.isinf()]) and got[seen.isnan()].isnan().all()
+    # keys: the rows behind a key of NaN have NaN, those before it are untouched
+    k[cu[1] + 100, 0, 3] = float("nan")
+    o2, lse2 = s2.prompt_fwd(q, k, v, cu)
+    _ok()
+    g = hq // hkv
+    rows = slice(cu[1] + 100, cu[2])
+    assert o2[rows, :g].isnan().all() and lse2[:g, rows].isnan().all()
+    keep = torch.ones(cu[-1], hq, dtype=torch.bool, device="cuda")
+    keep[rows, :g] = False
+    same = (o2 == o) | (o2.isnan() & o.isnan())
+    assert same[keep].all() and torch.equal(lse2[keep.T], lse[keep.T])
+
+
 def test_prompt_append_decode_agree():
     """A prompt through append and prompt_fwd, then its last row again as a decoding step: the same
     attention from the cache."""
