@@ -14,11 +14,11 @@
 // tokens' angles, shared by all heads through shared memory. The work then is units of one 16-byte
 // chunk of a head's first half and its partner D/2 columns on, for 4 tokens: 8 loads of 16 bytes in
 // flight a thread, 128 KB an SM, the first ones issued before the slots and angles are known. 4 tokens a
-// block where the heads give a block's threads work, 32 where they do not (fewer than half a block's
-// threads). A grid of few blocks splits the heads over its second axis.
+// block where the heads give a block's threads work, up to 32 where they do not, as many as give every
+// thread one unit. A grid of few blocks splits the heads over its second axis.
 // Measured (device time): 32768 tokens of 64 + 2 x 8 heads, d = 128: 217 us, 6.5 TB/s (8-token units and
-// blocks: 218 us, and 4.8 against 3.8 us for a batch of 64 tokens); 9830 tokens of 4 + 2 x 4 heads, d = 64:
-// 12.5 us, 2.8 TB/s, bound by the chain of lookups of a single wave of blocks.
+// blocks: 218 us, and 4.8 against 3.6 us for a batch of 64 tokens); 9830 tokens of 4 + 2 x 4 heads, d = 64:
+// 10.0 us, bound by the chain of lookups of a single wave of blocks.
 #pragma once
 
 #include "s2_serve_common.cuh"
@@ -27,6 +27,7 @@ namespace s2 {
 
 constexpr int kAppendUnit = 4;            // tokens of a work unit
 constexpr int kAppendThreads = 256;
+constexpr int kAppendMaxTokens = 32;      // of a block
 
 struct AppendParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -35,6 +36,7 @@ struct AppendParams {
   PagedRef kc, vc;
   const int *table, *cu, *lens;          // cu null: one token per sequence
   int T, B, Hq, Hkv, pages, page_size, max_pages;
+  int subs;                              // units of 4 tokens a block takes (of each head's chunk)
   unsigned int* err;
   unsigned long long turn[64];           // F_i
 };
@@ -49,24 +51,26 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
   return lo;
 }
 
-template <int D, int kTok>
+// kWide: p.subs units of 4 tokens a block, else one.
+template <int D, bool kWide>
 __global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kHalf = D / 2;
   constexpr int kChunks = D / 16;        // work items of a head: a 16-byte chunk and its partner
-  constexpr int kSubs = kTok / kAppendUnit;
+  constexpr int kTok = kWide ? kAppendMaxTokens : kAppendUnit;   // room in shared memory
+  const int subs = kWide ? p.subs : 1, tok = subs * kAppendUnit;
   __shared__ float s_cos[kTok][kHalf], s_sin[kTok][kHalf];
   __shared__ long long s_slot_k[kTok], s_slot_v[kTok];   // -1: not to be cached
   __shared__ int s_pos[kTok];                            // -1: to be skipped
   pdl_wait();
-  const int t_block = blockIdx.x * kTok;
-  const int items = (p.Hq + 2 * p.Hkv) * kChunks, units = items * kSubs;
+  const int t_block = blockIdx.x * tok;
+  const int items = (p.Hq + 2 * p.Hkv) * kChunks, units = items * subs;
   const int step = gridDim.y * kAppendThreads;
   int w = blockIdx.y * kAppendThreads + threadIdx.x;
 
   uint4 lo[kAppendUnit], hi[kAppendUnit];
   auto load = [&](int unit) {
-    const int item = kSubs == 1 ? unit : unit % items;
-    const int t0 = t_block + (kSubs == 1 ? 0 : unit / items * kAppendUnit);
+    const int sub = kWide ? unit / items : 0, item = unit - sub * items;
+    const int t0 = t_block + sub * kAppendUnit;
     const int h = item / kChunks, c = item % kChunks;
     const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
     const __nv_bfloat16* src = is_q ? p.q : is_k ? p.k : p.v;
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __gr
   if (w < units) load(w);
 
   // ---- the tokens' positions and slots, one lane each ----
-  if (threadIdx.x < kTok) {
+  if (threadIdx.x < tok) {
     const int t = t_block + threadIdx.x;
     long long pos = -1;
     int seq = t;
@@ -115,8 +119,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __gr
     s_pos[threadIdx.x] = pos < 0 ? -1 : pos > 0x7fffffff ? 0x7fffffff : static_cast<int>(pos);
   }
   __syncthreads();
-#pragma unroll
-  for (int k = threadIdx.x; k < kTok * kHalf; k += kAppendThreads) {
+  for (int k = threadIdx.x; k < tok * kHalf; k += kAppendThreads) {
     const int tt = k / kHalf, i = k % kHalf, pos = s_pos[tt];
     if (pos < 0) continue;
     const unsigned long long turns = static_cast<unsigned long long>(pos) * p.turn[i];
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __gr
 
   for (; w < units; w += step) {
     if (w >= step) load(w);
-    const int item = kSubs == 1 ? w : w % items, sub = kSubs == 1 ? 0 : w / items * kAppendUnit;
+    const int part = kWide ? w / items : 0, item = w - part * items, sub = part * kAppendUnit;
     const int h = item / kChunks, c = item % kChunks;
     const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
     const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;

@@ -141,18 +141,19 @@ const unsigned long long* turns(float base, float pi_scale, int d) {
   return last.f;
 }
 
-// 32 tokens a block where one token's heads would leave more than half of a block idle and the
-// tokens still fill the GPU; the heads split over the second axis until two blocks per SM exist.
+// Where one token's heads leave more than half of a block idle, a block takes as many groups of tokens as give
+// each thread one unit, but no more than leave two blocks per SM; the heads split over the second axis until
+// two blocks per SM exist.
 template <int D>
-s2attn_status launch_append(const s2::AppendParams& p, int num_sms, cudaStream_t stream) {
+s2attn_status launch_append(s2::AppendParams& p, int num_sms, cudaStream_t stream) {
   const int items = (p.Hq + 2 * p.Hkv) * (D / 16);
-  const bool wide = items <= s2::kAppendThreads / 2 && p.T >= 32 * num_sms;
-  const int tok = wide ? 32 : s2::kAppendUnit;
-  const int groups = (p.T - 1) / tok + 1;
-  const int most = (items * (tok / s2::kAppendUnit) + s2::kAppendThreads - 1) / s2::kAppendThreads;
+  p.subs = std::max(1, std::min({s2::kAppendThreads / items, s2::kAppendMaxTokens / s2::kAppendUnit,
+                                 p.T / (2 * num_sms * s2::kAppendUnit)}));
+  const int groups = (p.T - 1) / (p.subs * s2::kAppendUnit) + 1;
+  const int most = (items * p.subs + s2::kAppendThreads - 1) / s2::kAppendThreads;
   const dim3 grid(groups, std::max(1, std::min(most, 2 * num_sms / groups)));
   return launch_early("s2_append_kernel launch",
-                      wide ? s2::s2_append_kernel<D, 32> : s2::s2_append_kernel<D, s2::kAppendUnit>, grid,
+                      p.subs > 1 ? s2::s2_append_kernel<D, true> : s2::s2_append_kernel<D, false>, grid,
                       s2::kAppendThreads, 0, stream, p);
 }
 

@@ -164,14 +164,14 @@ def test_append_bad_page_and_length_are_reported_and_skipped():
         assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
 
 
-@pytest.mark.parametrize("hq,hkv,d,T", [(2, 1, 128, 5000), (4, 4, 64, 6001), (1, 1, 64, 4736)])
+@pytest.mark.parametrize("hq,hkv,d,T", [(2, 1, 128, 5000), (4, 4, 64, 6001), (1, 1, 64, 4736), (9, 3, 64, 3001)])
 def test_append_many_tokens_of_few_heads(hq, hkv, d, T):
-    """The form with 32 tokens a block, on views of one packed projection, ragged sequences, some of
+    """Blocks of several groups of tokens, on views of one packed projection, ragged sequences, some of
     them empty; rows behind the last sequence untouched."""
     r = random.Random(T)
     new = [0]
     while sum(new) < T - 200:
-        new.append(r.choice([0, 1, 31, 32, 33, 700]))
+        new.append(min(r.choice([0, 1, 31, 32, 33, 700]), T - sum(new)))
     T0, page = sum(new), 40
     rows, pages = _table(new, page, 4)
     packed = _randn(8, T, hq + 2 * hkv, d)
@@ -644,3 +644,82 @@ def test_append_without_queries_and_views_of_length_one():
         s2.decode(k, kc[:, :, :, :], vc, _ints([[0, 2]]), _ints([2]), scale=0.0)
     with pytest.raises(ValueError, match="contiguous"):
         s2.decode(big.transpose(1, 2)[:, :, :].reshape(4, 5, d).transpose(0, 1)[:, :, ::2], kc, vc, _ints([[0]] * 5), _ints([1] * 5))
+
+
+def test_steps_in_a_row_without_a_wait():
+    """Two hundred decoding steps queued one behind another, with no wait in between (each kernel may start
+    before the one in front of it has ended): the cache and the last outputs are those of the formula."""
+    hq, hkv, d, page, pi = 8, 2, 64, 16, 0.5
+    start, steps = [600, 5, 0, 130], 200
+    lens = [n + steps for n in start]
+    rows, pages = _table(lens, page, 8)
+    kc, vc = _randn(1, pages, page, hkv, d), _randn(2, pages, page, hkv, d)
+    kc0, vc0 = kc.clone(), vc.clone()
+    table, now = _ints(rows), _ints(start)
+    q, k, v = (_randn(3 + i, steps * 4, h, d).view(steps, 4, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    outs = []
+    for i in range(steps):
+        now += 1
+        q_rot, k_rot = s2.rope_append(q[i], k[i], v[i], kc, vc, table, now, pi_scale=pi)
+        outs.append((q_rot, k_rot, *s2.decode(q_rot, kc, vc, table, now)))
+    _ok()
+    for b, n in enumerate(start):
+        for i in range(steps):
+            kc0[rows[b][(n + i) // page], (n + i) % page] = outs[i][1][b]
+            vc0[rows[b][(n + i) // page], (n + i) % page] = v[i, b]
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+    for i in (0, 1, 57, 199):
+        q_rot, k_rot, o, lse = outs[i]
+        seen = [n + i + 1 for n in start]
+        _near_bf16(k_rot, _turn64(k[i], torch.tensor(seen, device="cuda") - 1, 10000.0, pi), 1.2e-5)
+        _check_decode(q_rot, kc, vc, rows, seen, d ** -0.5, o, lse)
+
+
+def test_decode_views_own_workspace_and_no_lse():
+    """q and o as views of wider buffers, a workspace full of NaN used by one call after another, no lse."""
+    hq, hkv, d, page = 12, 2, 128, 16
+    lens = [900, 3, 0, 2048]
+    rows, pages = _table(lens, page, 6)
+    kc, vc = _caches(11, pages, page, hkv, d, "kv_by_page")
+    packed, out = _randn(1, 4, 3 * hq, d), _randn(2, 4, 2 * hq, d)
+    q, o = packed[:, hq:2 * hq], out[:, hq:]
+    before = out.clone()
+    ws = torch.full((s2.s2attn_decode_workspace_size(4, hq, hkv, d),), 255, dtype=torch.uint8, device="cuda")
+    lse = torch.empty(4, hq, device="cuda")
+    table, n = _ints(rows), _ints(lens)
+    s2.s2attn_decode(q, kc, vc, table, n, o, lse, workspace=ws)
+    _ok()
+    _check_decode(q, kc, vc, rows, lens, d ** -0.5, o, lse)
+    assert torch.equal(out[:, :hq], before[:, :hq])
+    first = o.clone()
+    o.zero_()
+    s2.s2attn_decode(q, kc, vc, table, n, o, None, workspace=ws)
+    _ok()
+    assert torch.equal(o, first)
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.s2attn_decode(q, kc, vc, table, n, o, None, workspace=ws[:-256])
+
+
+def test_decode_of_thousands_of_sequences():
+    r = random.Random(1)
+    lens = [r.choice([0, 1, 15, 16, 17, 40]) for _ in range(3000)] + [3000]
+    hq, hkv, d, page = 2, 1, 64, 8
+    rows, pages = _table(lens, page, 2)
+    kc, vc = _randn(1, pages, page, hkv, d), _randn(2, pages, page, hkv, d)
+    q = _randn(3, len(lens), hq, d)
+    o, lse = s2.decode(q, kc, vc, _ints(rows), _ints(lens))
+    _ok()
+    pick = [i for i in range(0, 3000, 61)] + [2999, 3000]
+    at = torch.tensor(pick, device="cuda")
+    _check_decode(q[at], kc, vc, [rows[i] for i in pick], [lens[i] for i in pick], d ** -0.5, o[at], lse[at])
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert (o[empty] == 0).all() and (lse[empty] == float("-inf")).all() and o.isfinite().all()
+
+
+def test_prompts_of_no_rows():
+    q = _randn(1, 7, 2, 64)
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 7), 7.0, device="cuda")
+    for cu in ([0, 0], [3, 3, 3], [7, 7]):
+        s2.s2attn_prompt_fwd(q, q, q, o, lse, cu)
+    _ok()
+    assert (o == 7).all() and (lse == 7).all()
