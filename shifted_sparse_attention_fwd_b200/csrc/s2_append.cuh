@@ -9,7 +9,7 @@
 // the host, rounded once), and t * F_i modulo 2^64 is the exact fraction of a turn (error
 // t * 2^-64). Its upper 32 bits, as a signed number, are sincospif's argument.
 //
-// Memory bound: every element is read once and written once or twice. A block takes kTok tokens;
+// Memory bound: every element is read once and written once or twice. A block takes a few tokens;
 // one lane per token finds its sequence (binary search of cu_seqlens) and slot, and all threads the
 // tokens' angles, shared by all heads through shared memory. The work then is units of one 16-byte
 // chunk of a head's first half and its partner D/2 columns on, for 4 tokens: 8 loads of 16 bytes in

@@ -80,7 +80,7 @@ struct DecodeParams {
   int whole;                              // a CTA takes a whole segment
   FastDiv by_page;
   float scale_log2;
-  float* first_o;                         // [warps][rows][D]: pieces of a warp's first segment
+  float* first_o;                         // [warps][rows][D]: pieces of a warp's first segment (16 rows, D = 128)
   float* part_o;                          // [CTAs][2][rows][D]: partials of segments across CTAs
   float2* part_ml;                        // [CTAs][2][rows]: running maximum (log2 units), sum
   struct DecodeTail* tail;                // [CTAs]
@@ -88,12 +88,19 @@ struct DecodeParams {
   unsigned int* err;
 };
 
-template <int D>
+template <int D, int ROWS>
 struct DecodeLayout {
   static constexpr int kStages = 24 * 128 / (8 * D);      // 24 KB a warp
   static constexpr uint32_t kHalf = kDecodeTile * D * 2;  // the K or V rows of a tile
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr uint32_t kBytes = kDecodeWarps * kStages * kStage;
+  static constexpr uint32_t kRing = kDecodeWarps * kStages * kStage;
+  // The pieces of the warps' first segments stay in shared memory where it has room (a load from global memory
+  // takes 3 us while the other SMs stream), else they go to the workspace.
+  static constexpr uint32_t kFirst = ROWS * D * 4;        // of a warp
+  static constexpr bool kFirstShared = kRing + kDecodeWarps * kFirst <= 225 * 1024;
+  // (the list's prefix sums lie there before: 257 of 8 bytes)
+  static constexpr uint32_t kBytes = kRing + (kFirstShared ? kDecodeWarps * kFirst : 2304);
+  static_assert(kBytes + 3072 <= 227 * 1024 && kBytes - kRing >= 8 * (kDecodeThreads + 1), "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void decode_copy16(uint32_t dst, const void* src, bool on) {
@@ -130,11 +137,6 @@ __device__ __forceinline__ unsigned long long div_near(unsigned long long n, uns
   return n >> 32 ? n / d : static_cast<unsigned int>(n) / d;
 }
 
-template <int N>
-struct IntConst {
-  static constexpr int value = N;
-};
-
 // A tile: its sequence, head, number in the segment, and its place in the list.
 struct DecodeAt {
   int b, hv, tile, tiles, len;            // hv = kv head * chunks + chunk of its query heads
@@ -151,14 +153,17 @@ __device__ __forceinline__ int decode_heads(const DecodeParams& p, int hv, int& 
 // ROWS: 8 or 16 query rows a warp computes (the MMA has 16).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using L = DecodeLayout<D>;
+  using L = DecodeLayout<D, ROWS>;
   constexpr int kSteps = D / 16, kHalves = ROWS / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_pre[kDecodeThreads + 1], s_warp[kDecodeWarps];
+  __shared__ long long s_warp[kDecodeWarps];
+  long long* const s_pre = reinterpret_cast<long long*>(smem + L::kRing);
   // The pieces of segments that did not end where they began: of each warp's first segment and of
-  // its last. kind 0: none, 1: output in first_o, 2: in the warp's part of shared memory.
+  // its last. kind 0: none, 1: the first one's output, 2: the last one's, in the warp's ring.
   __shared__ struct { long long begin; int b, hv, tiles, kind; } s_piece[2 * kDecodeWarps];
   __shared__ float2 s_ml[2 * kDecodeWarps][ROWS];
+  __shared__ unsigned int s_segment[2 * kDecodeWarps];   // the pieces of each segment
+  __shared__ int s_segments;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_launch_dependents();
   pdl_wait();
@@ -255,6 +260,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     } while (a.tiles == 0);
   };
 
+  __syncthreads();                        // the prefix sums' place is free
+
   // ---- copies ----
   constexpr int kChunks = D / 8;                     // 16-byte chunks of a row
   constexpr int kRowsPer = 32 / kChunks;             // rows a warp copies with one instruction
@@ -310,6 +317,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     if (p.lse)
       for (int i = threadIdx.x; i < p.Hq; i += kDecodeThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
   }
+
+  // Where a warp leaves the piece of its first segment.
+  auto first_piece = [&](int w) -> float* {
+    if (L::kFirstShared) return reinterpret_cast<float*>(smem + L::kRing + w * L::kFirst);
+    return p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + w) * p.rows * D;
+  };
 
   // ---- the range, tile by tile ----
   const int r0 = lane / 4, c0 = 2 * (lane % 4);
@@ -425,7 +438,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     }
     const bool whole = seg_end && seg_tile == 0;
     const int piece = 2 * warp + (end ? 1 : 0);
-    float* out = p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + warp) * p.rows * D;
+    float* out = first_piece(warp);
     if (!whole) {
       if (end) {                                     // the ring is free: every tile has been used
         __syncwarp();
@@ -465,88 +478,71 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
-  // ---- join the CTA's pieces, segment by segment ----
-  // (one or two segments: by all threads; more of them, of few pieces each: by a warp each)
-  // Lane x looks at piece x: `live` are the pieces there are, `heads` the first ones of their segments.
-  const bool is_piece = lane < 2 * kDecodeWarps && s_piece[lane & (2 * kDecodeWarps - 1)].kind != 0;
-  const long long my_begin = s_piece[lane & (2 * kDecodeWarps - 1)].begin;
-  const unsigned int live = __ballot_sync(0xffffffffu, is_piece);
-  const unsigned int before = live & ((1u << lane) - 1u);
-  const long long last_begin = __shfl_sync(0xffffffffu, my_begin, before ? 31 - __clz(before) : 0);
-  const unsigned int heads = __ballot_sync(0xffffffffu, is_piece && (before == 0 || last_begin != my_begin));
-  const bool by_warp = __popc(heads) > 2;
-  const int rank = by_warp ? lane : threadIdx.x;
-  int g = 0;
-  for (unsigned int todo = heads; todo; todo &= todo - 1, ++g) {
-    if (by_warp && g % kDecodeWarps != warp) continue;
-    const int i = __ffs(todo) - 1;
-    const unsigned int rest = todo & (todo - 1);
-    // the segment's pieces
-    const unsigned int mine = live & ~((1u << i) - 1u) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xffffffffu);
+  // ---- join the CTA's pieces ----
+  // Lane x of the first warp looks at piece x: `live` are the pieces there are, `heads` the first ones of
+  // their segments; each head notes its segment's pieces.
+  if (warp == 0) {
+    const int x = lane & (2 * kDecodeWarps - 1);
+    const bool is_piece = lane < 2 * kDecodeWarps && s_piece[x].kind != 0;
+    const long long begin = s_piece[x].begin;
+    const unsigned int live = __ballot_sync(0xffffffffu, is_piece);
+    const unsigned int before = live & ((1u << lane) - 1u);
+    const long long last_begin = __shfl_sync(0xffffffffu, begin, before ? 31 - __clz(before) : 0);
+    const bool head = is_piece && (before == 0 || last_begin != begin);
+    const unsigned int heads = __ballot_sync(0xffffffffu, head);
+    const unsigned int behind = heads & ~((2u << lane) - 1u);
+    if (head)
+      s_segment[__popc(heads & ((1u << lane) - 1u))] =
+          live & ~((1u << lane) - 1u) & (behind ? (1u << (__ffs(behind) - 1)) - 1u : 0xffffffffu);
+    if (lane == 0) s_segments = __popc(heads);
+  }
+  __syncthreads();
+  // Four columns of a row of a segment each time, all segments side by side.
+  const int places_each = p.rows * (D / 4);
+#pragma unroll 1
+  for (int u = threadIdx.x; u < s_segments * places_each; u += kDecodeThreads) {
+    const int g = u / places_each, in = u - g * places_each;
+    const int row = in / (D / 4), col = 4 * (in % (D / 4));
+    const unsigned int mine = s_segment[g];
+    const int i = __ffs(mine) - 1;
     const long long begin = s_piece[i].begin;
     const int b = s_piece[i].b, hv = s_piece[i].hv, tiles = s_piece[i].tiles;
     int h0;
-    const int rows = decode_heads(p, hv, h0);
+    if (row >= decode_heads(p, hv, h0)) continue;
+    float mt = -INFINITY, lt = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (unsigned int m = mine; m; m &= m - 1) {
+      const int k = __ffs(m) - 1;
+      const float* src = s_piece[k].kind == 1
+          ? first_piece(k / 2)
+          : reinterpret_cast<const float*>(smem + (k / 2) * (L::kStages * L::kStage));
+      const float4 v = *reinterpret_cast<const float4*>(src + row * D + col);
+      const float2 ml = s_ml[k][row];
+      const float mn = fmaxf(mt, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+      const float alpha = fast_exp2(mt - mu), w = fast_exp2(ml.x - mu);
+      mt = mn;
+      lt = lt * alpha + ml.y * w;
+      sum.x = sum.x * alpha + v.x * w;
+      sum.y = sum.y * alpha + v.y * w;
+      sum.z = sum.z * alpha + v.z * w;
+      sum.w = sum.w * alpha + v.w * w;
+    }
     const bool starts = begin >= cta_first, ends = begin + tiles <= cta_last;
-    // kTeam threads, 4 columns of a row at a time, all of a thread's places of a piece loaded at once
-    auto join = [&](auto team) {
-      constexpr int kTeam = decltype(team)::value;
-      constexpr int kPlaces = (ROWS * (D / 4) + kTeam - 1) / kTeam;
-      float4 sum[kPlaces];
-      float mt[kPlaces], lt[kPlaces];
-#pragma unroll
-      for (int x = 0; x < kPlaces; ++x) {
-        const int row = min((rank + kTeam * x) / (D / 4), rows - 1);
-        mt[x] = -INFINITY;
-        lt[x] = 0.f;
-        sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (unsigned int m = mine; m; m &= m - 1) mt[x] = fmaxf(mt[x], s_ml[__ffs(m) - 1][row].x);
-      }
-      for (unsigned int m = mine; m; m &= m - 1) {
-        const int k = __ffs(m) - 1;
-        const float* src = s_piece[k].kind == 1
-            ? p.first_o + (static_cast<long long>(blockIdx.x) * kDecodeWarps + k / 2) * p.rows * D
-            : reinterpret_cast<const float*>(smem + (k / 2) * (L::kStages * L::kStage));
-        float4 v[kPlaces];
-#pragma unroll
-        for (int x = 0; x < kPlaces; ++x) {
-          const int u = rank + kTeam * x, row = min(u / (D / 4), rows - 1);
-          v[x] = *reinterpret_cast<const float4*>(src + row * D + 4 * (u % (D / 4)));
-        }
-#pragma unroll
-        for (int x = 0; x < kPlaces; ++x) {
-          const int row = min((rank + kTeam * x) / (D / 4), rows - 1);
-          const float2 ml = s_ml[k][row];
-          const float w = fast_exp2(ml.x - (mt[x] == -INFINITY ? 0.f : mt[x]));
-          lt[x] = fmaf(ml.y, w, lt[x]);
-          sum[x].x = fmaf(v[x].x, w, sum[x].x);
-          sum[x].y = fmaf(v[x].y, w, sum[x].y);
-          sum[x].z = fmaf(v[x].z, w, sum[x].z);
-          sum[x].w = fmaf(v[x].w, w, sum[x].w);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < kPlaces; ++x) {
-        const int u = rank + kTeam * x, row = u / (D / 4), col = 4 * (u % (D / 4));
-        if (row >= rows) continue;
-        if (starts && ends) {
-          const float inv = 1.f / lt[x];
-          uint2 w2;
-          w2.x = pack_bf16(sum[x].x * inv, sum[x].y * inv);
-          w2.y = pack_bf16(sum[x].z * inv, sum[x].w * inv);
-          *reinterpret_cast<uint2*>(p.o + b * p.o_sb + static_cast<long long>(h0 + row) * D + col) = w2;
-          if (p.lse && col == 0)
-            p.lse[static_cast<long long>(b) * p.Hq + h0 + row] = (mt[x] + log2f(lt[x])) * 0.6931471805599453f;
-        } else {
-          const long long part = (blockIdx.x * 2ll + (starts ? 1 : 0)) * p.rows + row;
-          *reinterpret_cast<float4*>(p.part_o + part * D + col) = sum[x];
-          if (col == 0) p.part_ml[part] = make_float2(mt[x], lt[x]);
-        }
-      }
-    };
-    if (by_warp) join(IntConst<32>{});
-    else join(IntConst<kDecodeThreads>{});
-    if (starts && !ends && rank == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
+    if (starts && ends) {
+      const float inv = 1.f / lt;
+      uint2 w2;
+      w2.x = pack_bf16(sum.x * inv, sum.y * inv);
+      w2.y = pack_bf16(sum.z * inv, sum.w * inv);
+      *reinterpret_cast<uint2*>(p.o + b * p.o_sb + static_cast<long long>(h0 + row) * D + col) = w2;
+      if (p.lse && col == 0)
+        p.lse[static_cast<long long>(b) * p.Hq + h0 + row] = (mt + log2f(lt)) * 0.6931471805599453f;
+    } else {
+      const long long part = (blockIdx.x * 2ll + (starts ? 1 : 0)) * p.rows + row;
+      *reinterpret_cast<float4*>(p.part_o + part * D + col) = sum;
+      if (col == 0) p.part_ml[part] = make_float2(mt, lt);
+      if (starts && in == 0) p.tail[blockIdx.x] = DecodeTail{begin, cta_range, b, hv, tiles, 1};
+    }
   }
 }
 

@@ -38,10 +38,10 @@ ServeDevice g_serve_dev[kMaxDevices];
 template <int D>
 cudaError_t serve_smem_attrs() {
   cudaError_t e = cudaFuncSetAttribute(
-      s2::s2_decode_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2::DecodeLayout<D>::kBytes);
+      s2::s2_decode_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2::DecodeLayout<D, 8>::kBytes);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(s2::s2_decode_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           s2::DecodeLayout<D>::kBytes);
+                           s2::DecodeLayout<D, 16>::kBytes);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(s2::s2_prompt_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            s2::PromptLayout<D>::kLaunchBytes);
@@ -173,7 +173,7 @@ template <int D>
 s2attn_status launch_decode(const s2::DecodeParams& p, int grid, cudaStream_t stream) {
   const s2attn_status s = launch_early(
       "s2_decode_kernel launch", p.rows <= 8 ? s2::s2_decode_kernel<D, 8> : s2::s2_decode_kernel<D, 16>, dim3(grid),
-      s2::kDecodeThreads, s2::DecodeLayout<D>::kBytes, stream, p);
+      s2::kDecodeThreads, p.rows <= 8 ? s2::DecodeLayout<D, 8>::kBytes : s2::DecodeLayout<D, 16>::kBytes, stream, p);
   if (s != S2ATTN_OK || grid == 1 || p.whole) return s;   // one CTA, or whole segments: nothing crosses CTAs
   return launch_early("s2_decode_join_kernel launch", s2::s2_decode_join_kernel<D>, dim3(grid - 1, p.rows),
                       s2::kDecodeJoinThreads, 0, stream, p);
