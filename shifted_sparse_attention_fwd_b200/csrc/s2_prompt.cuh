@@ -33,7 +33,9 @@
 // O and l are rescaled.
 //
 // Measured, in a loop: one prompt of 8192 tokens, 32 heads, d = 128: 0.55 ms, 1.0 PFLOP/s of visible work; 39k
-// tokens in two prompts, 64 / 8 heads: 1.09 PFLOP/s; 12 prompts of 1 to 4999 tokens, 32 heads: 0.263 ms, 0.85.
+// tokens in two prompts, 64 / 8 heads: 1.09 PFLOP/s; 12 prompts of 1 to 4999 tokens, 32 heads: 0.263 ms, 0.85; 64 prompts of
+// 128 tokens, 32 heads: 49 us, 5.5 TB/s (there the loads' latency and the memory bound it, and what a short unit costs
+// in sequence: 200 prompts of 40, 109 us).
 // Tensor pipe and exponential unit are each a good half busy at 1.7 GHz: the GPU sits at its power cap (990 W),
 // and a pass over the 8192 tokens takes 0.54 J, of which the MMAs alone need 0.36 (the same launch with the
 // softmax left out) and cuBLAS 0.39 for as many flops: energy, not a pipe, bounds it. Scores are loaded 16
@@ -42,11 +44,13 @@
 // epilogue (128 registers a thread at launch spill the softmax: 0.79 ms), turns taken by the MMA issuers
 // instead of the softmax (0.59 ms).
 //
-// Masked places hold anything. Keys are masked by selection. Values would reach a product as 0 * NaN: rows
-// of other sequences are not loaded (the last V tile of a sequence is filled up with zeros), and warp 11
-// looks through the diagonal V tiles, which hold rows that some query rows do not see: infinities and NaN
-// are replaced by zeros there, and in such a unit, a rare one, the warp adds them to the stored rows that
-// do see them. (8192 tokens: no time; it has a step's time to look at 32 KB.)
+// Masked places hold anything. Keys are masked by selection. Values would reach a product as 0 * NaN: warp 11
+// looks through the diagonal V tiles, which hold rows that some query rows do not see, and, where a sequence
+// ends inside the tile (its last tile is always a diagonal one), rows behind it that none sees: infinities and
+// NaN are replaced by zeros there, and in a unit whose own rows held some, a rare one, the warp adds them to the
+// stored rows that do see them. (8192 tokens: no time; it has a step's time to look at 32 KB. Rows behind the
+// end kept out by loads in boxes of 8 rows instead: a prompt of 40 tokens spent 4100 of its unit's 6100 cycles
+// on their issue.)
 #pragma once
 
 #include "s2_common.cuh"
@@ -251,9 +255,8 @@ __device__ __forceinline__ void softmax_row(uint32_t s_col, uint32_t (&a)[16], u
 template <int D, bool kHeads>
 __global__ void __launch_bounds__(384, 1)
     s2_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV8,
-                     const __grid_constant__ CUtensorMap tmO8, const __grid_constant__ PromptParams p,
-                     const __grid_constant__ PromptWork work) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO8,
+                     const __grid_constant__ PromptParams p, const __grid_constant__ PromptWork work) {
   using L = PromptLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = aligned_smem(smem_raw);
@@ -327,6 +330,23 @@ __global__ void __launch_bounds__(384, 1)
     int clc_asked = -1;                   // the last request's number
     bool ok = true, clc_open = false;
     PromptUnit u = prompt_unit<kHeads>(p, work, blockIdx.x);
+    // A unit of one tile only (a prompt's odd last rows; each unit of prompts of up to 128 tokens) goes to the
+    // tile that the unit before left free, so that two such units are on their way at a time: 200 prompts of
+    // 40 tokens, 32 heads, 109 against 162 us.
+    int last = -1;                        // the tile that the last unit had to itself
+    auto place = [&]() {
+      if (kHeads || u.n[1] != 0) {
+        last = -1;
+        return;
+      }
+      last = last == 0 ? 1 : 0;
+      if (last == 1) {
+        u.n[1] = u.n[0];
+        u.qt[1] = u.qt[0];
+        u.n[0] = 0;
+      }
+    };
+    place();
     auto load_box = [&](uint32_t dst, const CUtensorMap* m, int b, int h, int row) {
       if (lane == 0) {
         mbar_expect_tx(bar(b), Tile<D>::kBytes);
@@ -347,37 +367,7 @@ __global__ void __launch_bounds__(384, 1)
       const int i = v_issued, st = i % L::kStages;
       if (i >= L::kStages && !warp_wait(bar(L::B_VE + st), ((i / L::kStages) - 1) & 1, ctx, 2)) return false;
       const uint32_t dst = sbase + L::kV + st * L::kTile;
-      const int valid = u.len - j * kTileRows, row0 = u.start + j * kTileRows;
-      if (valid >= kTileRows) {
-        load_box(dst, &tmV, L::B_V + st, u.kvh, row0);
-      } else {
-        // The sequence ends inside the tile: whole 8-row atoms by TMA, the one that the end cuts by
-        // the warp's own copies, and zeros (rows out of the tensor's bounds) behind it.
-        const int whole = valid / 8, cut = valid % 8;
-        if (cut) {
-          constexpr int kChunks = D / 8;
-          for (int x = lane; x < 8 * kChunks; x += 32) {
-            const int r = x / kChunks, c = x % kChunks, row = 8 * whole + r;
-            cp_async16(dst + (c / 8) * Tile<D>::kHalfBytes + row * 128 + (((c % 8) ^ (row & 7)) * 16),
-                       p.v + (row0 + (r < cut ? row : 0)) * p.v_st + static_cast<long long>(u.kvh) * D + 8 * c,
-                       r < cut ? 16u : 0u);
-          }
-          cp_async_wait_all();
-          fence_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
-          mbar_expect_tx(bar(L::B_V + st), Tile<D>::kBytes - (cut ? 8 * 128 * Tile<D>::kHalves : 0));
-          for (int a = 0; a < kTileRows / 8; ++a) {
-            if (cut && a == whole) continue;
-#pragma unroll
-            for (int half = 0; half < Tile<D>::kHalves; ++half)
-              tma_load_4d(dst + half * Tile<D>::kHalfBytes + a * 1024, &tmV8, bar(L::B_V + st), half * 64, u.kvh,
-                          a < whole ? row0 + 8 * a : p.T, 0);
-          }
-        }
-        __syncwarp();
-      }
+      load_box(dst, &tmV, L::B_V + st, u.kvh, u.start + j * kTileRows);
       ++v_issued;
       return true;
     };
@@ -427,8 +417,12 @@ __global__ void __launch_bounds__(384, 1)
       const int next = clc_answer(sbase + L::kClc);
       __syncwarp();
       fence_async_smem();                 // read before the next request may write
-      if (next >= 0) u = prompt_unit<kHeads>(p, work, next);
-      else u.live = 0;
+      if (next >= 0) {
+        u = prompt_unit<kHeads>(p, work, next);
+        place();
+      } else {
+        u.live = 0;
+      }
       ok = publish(k + 1);
     }
     // Every issued copy lands before the CTA can exit.
@@ -455,19 +449,29 @@ __global__ void __launch_bounds__(384, 1)
         const int diag = (j + 1 == u.n[0] ? 1 : 0) | (j + 1 == u.n[1] ? 2 : 0);
         if (diag) {
           uint4* tile = reinterpret_cast<uint4*>(smem + L::kV + st * L::kTile);
-          uint32_t seen = 0;
-#pragma unroll 4
+          // 0 * x summed over the tile: NaN if some x is infinite or NaN. Only then a closer look.
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+#pragma unroll 8
           for (int x = lane; x < static_cast<int>(L::kTile / 16); x += 32) {
-            const uint4 w = tile[x];
-            seen |= bf16x2_not_finite(w.x) | bf16x2_not_finite(w.y) | bf16x2_not_finite(w.z) | bf16x2_not_finite(w.w);
+            uint4 w = tile[x];
+            sum[0] = __hfma2(reinterpret_cast<__nv_bfloat162&>(w.x), zero, sum[0]);
+            sum[1] = __hfma2(reinterpret_cast<__nv_bfloat162&>(w.y), zero, sum[1]);
+            sum[2] = __hfma2(reinterpret_cast<__nv_bfloat162&>(w.z), zero, sum[2]);
+            sum[3] = __hfma2(reinterpret_cast<__nv_bfloat162&>(w.w), zero, sum[3]);
           }
-          if (__any_sync(0xffffffffu, seen != 0)) {
-            bad |= diag;
+          const float2 found = __bfloat1622float2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
+          if (__any_sync(0xffffffffu, !(found.x + found.y == 0.f))) {
+            const int valid = u.len - j * kTileRows;   // rows of the sequence in the tile
+            uint32_t seen = 0;
             for (int x = lane; x < static_cast<int>(L::kTile / 16); x += 32) {
               const uint4 w = tile[x];
+              if (x / 8 % kTileRows < valid)
+                seen |= bf16x2_not_finite(w.x) | bf16x2_not_finite(w.y) | bf16x2_not_finite(w.z) | bf16x2_not_finite(w.w);
               tile[x] = make_uint4(bf16x2_finite_part(w.x), bf16x2_finite_part(w.y), bf16x2_finite_part(w.z),
                                    bf16x2_finite_part(w.w));
             }
+            if (__any_sync(0xffffffffu, seen != 0)) bad |= diag;
             fence_async_smem();           // the MMAs read the tile through the async proxy
           }
           __syncwarp();
@@ -565,19 +569,22 @@ __global__ void __launch_bounds__(384, 1)
       // epilogue, and the ring's slot released after it.
       const int slot = ku % kUnitRing;
       if (!warp_wait(bar(L::B_UF + slot), (ku / kUnitRing) & 1, ctx, 11) || !ring[slot].live) break;
-      const int n = ring[slot].n[wg], n_all = max(ring[slot].n[0], ring[slot].n[1]);
+      const int n = ring[slot].n[wg], n_other = ring[slot].n[wg ^ 1];
+      const bool turns = kHeads || (n != 0 && n_other != 0);     // a unit of one tile only takes none
+      const int n_all = turns ? max(n, n_other) : n;
       float m_run = -INFINITY, l_run = 0.f;
       // The two tiles' passes take turns (tile 0's pass k, tile 1's pass k, tile 0's k + 1, ...): each then
       // has the exponential units to itself while the other tile's MMAs run. Left alone, both warpgroups
       // fall into step, and their MMAs too: 666 against 549 us on one 8192-token prompt of 32 heads.
       auto my_turn = [&]() -> bool {
+        if (!turns) return true;
         const int k = wg == 0 ? turn - 1 : turn;     // the other tile's pass that has to be over
         ++turn;
         return k < 0 || warp_wait(bar(L::B_TURN + (wg ^ 1)), k & 1, ctx, 15);
       };
       auto pass_turn = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::B_TURN + wg));
+        if (turns && lane == 0) mbar_arrive(bar(L::B_TURN + wg));
       };
       for (int j = 0; j < n_all; ++j) {
         if (j >= n) {                                // no pass of this tile here

@@ -199,7 +199,7 @@ constexpr long long kPromptL2Bytes = 64ll << 20;
 
 // One launch per kPromptMaxSeqs sequences and kPromptMaxTiles query tiles.
 template <int D>
-s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[5], const int* cu, int n_seqs,
+s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[4], const int* cu, int n_seqs,
                             cudaStream_t stream) {
   static thread_local s2::PromptWork work;
   static thread_local std::vector<int> order;
@@ -214,8 +214,8 @@ s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[5], c
     const unsigned grid = static_cast<unsigned>(p.Hkv) * per_kv * p.n_tiles;
     const s2attn_status s = launch_early(
         "s2_prompt_kernel launch", heads ? s2::s2_prompt_kernel<D, true> : s2::s2_prompt_kernel<D, false>, dim3(grid),
-        s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes, stream, maps[0], maps[1], maps[2], maps[3],
-        maps[4], p, work);
+        s2::PromptLayout<D>::kThreads, s2::PromptLayout<D>::kLaunchBytes, stream, maps[0], maps[1], maps[2], maps[3], p,
+        work);
     p.n_tiles = 0;
     return s;
   };
@@ -385,12 +385,11 @@ s2attn_status s2attn_prompt_fwd(const void* q, const void* k, const void* v, voi
     st[i] = strides ? strides[i] : static_cast<long long>(head_count[i]) * d;
     if (bad_row_stride(st[i], head_count[i], d)) return S2ATTN_ERR_INVALID_ARG;
   }
-  CUtensorMap maps[5];
+  CUtensorMap maps[4];
   if ((s = encode_rows(&maps[0], q, T, Hq, d, s2::kTileRows, st[0])) != S2ATTN_OK) return s;
   if ((s = encode_rows(&maps[1], k, T, Hkv, d, s2::kPromptKeys, st[1])) != S2ATTN_OK) return s;
   if ((s = encode_rows(&maps[2], v, T, Hkv, d, s2::kPromptKeys, st[2])) != S2ATTN_OK) return s;
-  if ((s = encode_rows(&maps[3], v, T, Hkv, d, 8, st[2])) != S2ATTN_OK) return s;
-  if ((s = encode_rows(&maps[4], o, T, Hq, d, 8, st[3])) != S2ATTN_OK) return s;
+  if ((s = encode_rows(&maps[3], o, T, Hq, d, 8, st[3])) != S2ATTN_OK) return s;
   s2::PromptParams p{};
   p.v = static_cast<const __nv_bfloat16*>(v);
   p.v_st = st[2];

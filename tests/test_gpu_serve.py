@@ -479,6 +479,38 @@ def test_prompt_values_of_hidden_rows(hq, hkv, d):
     assert same[keep].all() and torch.equal(lse2[keep.T], lse[keep.T])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(3, 3, 128), (9, 3, 64), (4, 2, 128)])
+def test_prompts_of_a_few_tokens_by_the_hundred(hq, hkv, d):
+    """Units of one query tile and of two, many for each CTA, in any order: right, and the values that a row
+    does not see (of its own sequence, and of the neighbour that shares its tile of values) never reach it."""
+    lens = [40, 128, 1, 130, 256, 300, 7, 390, 16, 127, 64, 129] * 20
+    cu = _cu(lens)
+    q, k, v = (_randn(50 + i, cu[-1], h, d) for i, h in enumerate((hq, hkv, hkv)))
+    o, lse = s2.prompt_fwd(q, k, v, cu)
+    _ok()
+    want, want_lse, mean_abs = _prompt64(q, k, v, cu, d ** -0.5)
+    _near_bf16(o, want, (BF16_STEP + 1e-5) * mean_abs)
+    assert float((lse.double() - want_lse).abs().max()) <= 2e-5
+    sign = torch.zeros(cu[-1], hkv, d, dtype=torch.float64, device="cuda")
+    for i, n in enumerate(lens):
+        for r, x in ((0, "inf"), (n - 1, "nan"), (n // 2, "-inf")) if i % 5 == 2 else ():
+            v[cu[i] + r, (i + r) % hkv, (7 * i + r) % d] = float(x)
+        a, e = cu[i], cu[i + 1]
+        sign[a:e] = torch.where(v[a:e].isfinite(), torch.zeros_like(v[a:e]), v[a:e]).double().cumsum(0)
+    o2, lse2 = s2.prompt_fwd(q, k, v, cu)
+    _ok()
+    assert torch.equal(lse2, lse)
+    seen = sign.repeat_interleave(hq // hkv, 1)
+    hit = ~(seen == 0)
+    dirty = torch.zeros(cu[-1], dtype=torch.bool, device="cuda")
+    for i in range(2, len(lens), 5):
+        dirty[cu[i]:cu[i + 1]] = True
+    assert torch.equal(o2[~dirty], o[~dirty])
+    got = o2.double()
+    assert got[~hit].isfinite().all()
+    assert torch.equal(got[seen.isinf()], seen[seen.isinf()]) and got[seen.isnan()].isnan().all()
+
+
 def test_prompt_append_decode_agree():
     """A prompt through append and prompt_fwd, then its last row again as a decoding step: the same
     attention from the cache."""
