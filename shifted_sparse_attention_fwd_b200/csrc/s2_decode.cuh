@@ -434,10 +434,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) s2_decode_kernel(const __gr
     if (!seg_end && !end) continue;
     fresh = true;
     if (ROWS == 8) {
+      // (where a value was infinite the product with the rounded P is the result: the rest of P may be 0 or
+      // negative, and its product NaN or of the other sign)
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
-        acc[j][0] += acc[j][2];
-        acc[j][1] += acc[j][3];
+        if (isfinite(acc[j][0])) acc[j][0] += acc[j][2];
+        if (isfinite(acc[j][1])) acc[j][1] += acc[j][3];
       }
     }
     const bool whole = seg_end && seg_tile == 0;

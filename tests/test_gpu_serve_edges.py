@@ -1,0 +1,53 @@
+"""The serving operators on the GPU where a call is unusual. Tolerances as derived in test_gpu_serve.py, whose
+helpers are used."""
+import ctypes
+
+import pytest
+import torch
+
+import shifted_sparse_attention_fwd_b200 as s2
+from test_gpu_serve import (BF16_STEP, _caches, _check_decode, _cu, _decode64, _ints, _near_bf16, _ok, _prompt64,
+                            _randn, _table, _turn64)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s2.lib()
+
+
+# ------------------------------------------------------------------------------------------
+# infinities and NaN in values that a row sees
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 128), (8, 1, 64), (16, 2, 128), (9, 1, 64), (16, 1, 128), (17, 1, 64)])
+@pytest.mark.parametrize("lens", [[1, 40, 300], [9000, 0, 77], [700] * 5])
+def test_decode_infinite_and_nan_values(hq, hkv, d, lens):
+    """A seen value of +inf makes its column +inf for every group size, opposite infinities and NaN make it NaN,
+    and no other column moves. (Scores are small, so no weight underflows.)"""
+    page = 16
+    rows, pages = _table(lens, page, 7)
+    kc, vc = _randn(1, pages, page, hkv, d), _randn(2, pages, page, hkv, d)
+    q = _randn(3, len(lens), hq, d)
+    table, n = _ints(rows), _ints(lens)
+    want, want_lse = s2.decode(q, kc, vc, table, n)
+    seen = torch.zeros(len(lens), hkv, d, dtype=torch.float64, device="cuda")
+    for b, m in enumerate(lens):
+        # (token, column, value): first and last token, the middle one, two of opposite signs
+        for t, c, x in ((0, 0, "inf"), (m - 1, 1, "inf"), (m // 2, 2, "-inf"), (m // 3, d - 1, "nan"), (0, 5, "inf"),
+                        (m - 1, 5, "-inf" if m > 1 else "inf"), (m // 2, 8, "inf"), (m // 4, 8, "inf")):
+            if m:
+                h = (b + c) % hkv
+                if vc[rows[b][t // page], t % page, h, c].isfinite():
+                    vc[rows[b][t // page], t % page, h, c] = float(x)
+                    seen[b, h, c] += float(x)
+    o, lse = s2.decode(q, kc, vc, table, n)
+    _ok()
+    assert torch.equal(lse, want_lse)
+    seen = seen.repeat_interleave(hq // hkv, 1)
+    clean = seen == 0
+    assert torch.equal(o[clean], want[clean])
+    got = o.double()
+    assert torch.equal(got[seen.isinf()], seen[seen.isinf()]) and got[seen.isnan()].isnan().all()
