@@ -384,8 +384,10 @@ S2ATTN_API s2attn_status s2attn_rope_pi(const void* x, void* y, int B, int N, in
  * s2attn_rope_pi, but exact to fp32 rounding of sine and cosine at any position); turned queries
  * go to q_rot, turned keys to the cache and, if not NULL, to k_rot, values to the cache.
  * q_rot may be q, k_rot may be k; no other overlap. q and q_rot may both be NULL. Rows behind
- * the last sequence, rows before the first and rows whose position would be negative (idle rows:
- * cache_lens = 0) are skipped: nothing is written for them. Two tokens must not share a slot.
+ * the last sequence, rows before the first and rows of an idle sequence (cache_lens = 0) are
+ * skipped: nothing is written for them. So are rows whose position would be negative (a length below
+ * 0, or smaller than the sequence's new rows), and those are reported as a bad length. The length of a
+ * sequence without new rows is not looked at. Two tokens must not share a slot.
  * `strides`: NULL or {q, q_rot, k, k_rot, v row strides, k_cache sp, st, v_cache sp, st}. Row
  * strides are multiples of 8 and at least heads * d. Errors as above, plus base <= 1, pi_scale <=
  * 0 -> S2ATTN_ERR_INVALID_ARG; max_pages * page_size > 2^31 - 129 -> S2ATTN_ERR_UNSUPPORTED.

@@ -90,15 +90,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) s2_append_kernel(const __gr
   if (threadIdx.x < tok) {
     const int t = t_block + threadIdx.x;
     long long pos = -1;
-    int seq = t;
+    int seq = t, len = 0;
     if (t < p.T) {
       if (p.cu) {
         seq = find_sequence(p.cu, p.B, t);
-        if (seq < p.B && t >= p.cu[seq])
-          pos = static_cast<long long>(p.lens[seq]) - p.cu[seq + 1] + t;
+        if (seq < p.B && t >= p.cu[seq]) {
+          len = p.lens[seq];
+          pos = static_cast<long long>(len) - p.cu[seq + 1] + t;
+        }
       } else {
-        pos = static_cast<long long>(p.lens[seq]) - 1;
+        len = p.lens[seq];
+        pos = static_cast<long long>(len) - 1;
       }
+      // a row without a position: of an idle sequence if the length is 0, else of a length that cannot be
+      if (pos < 0 && len != 0) report_bad_index(p.err, KID_APPEND, kSiteBadLength);
     }
     long long sk = -1, sv = -1;
     if (pos >= static_cast<long long>(p.max_pages) * p.page_size) {

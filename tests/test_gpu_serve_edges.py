@@ -85,3 +85,41 @@ def test_prompt_of_nothing_but_infinite_values(hq, hkv, d, x):
     assert o.isnan().all() if x == "nan" else (o == float(x)).all()
     # a unit's 256 rows are read and written once more, by one warp: about 40 us beside its 10 to 20
     assert full <= 16 * plain + 50, (plain, full)
+
+
+# ------------------------------------------------------------------------------------------
+# lengths and pages outside the cache
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,cu,skipped", [
+    ([3, -1], None, [1]),                        # one token each, a negative length
+    ([3, -(1 << 31)], None, [1]),
+    ([3, -5], [0, 2, 5], [2, 3, 4]),             # several rows of a sequence of a negative length
+    ([3, 2], [0, 2, 5], [2]),                    # a length that leaves the new rows out: the first has no position
+    ([3, 1], [0, 2, 5], [2, 3]),
+])
+def test_append_reports_lengths_too_small_for_the_rows(lens, cu, skipped):
+    """Rows without a position are skipped, and reported unless the sequence is idle (length 0)."""
+    page, hq, hkv, d = 8, 4, 2, 64
+    T = cu[-1] if cu else 2
+    q, k, v = (_randn(1 + i, T, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    kc, vc = _randn(4, 2, page, hkv, d), _randn(5, 2, page, hkv, d)
+    kc0, vc0 = kc.clone(), vc.clone()
+    q_rot, k_rot = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    table = _ints([[0], [1]])
+    args = (q, q_rot, k, k_rot, v, kc, vc, table)
+    cu_dev = None if cu is None else _ints(cu)
+    s2.s2attn_rope_append(*args, _ints(lens), cu_dev)
+    torch.cuda.synchronize()
+    assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (6 << 8) | 0x81)
+    rows = [(s, t) for s in range(2) for t in (range(cu[s], cu[s + 1]) if cu else [s])]
+    for s, t in rows:
+        if t in skipped:
+            assert (q_rot[t] == 7).all() and (k_rot[t] == 7).all()
+            continue
+        pos = lens[s] - (cu[s + 1] if cu else s + 1) + t
+        kc0[s, pos], vc0[s, pos] = k_rot[t], v[t]
+        _near_bf16(k_rot[t:t + 1], _turn64(k[t:t + 1], torch.tensor([pos], device="cuda"), 10000.0, 1.0), 1.2e-5)
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+    # an idle sequence is no error
+    s2.s2attn_rope_append(*args, _ints([3, 0]), cu_dev)
+    _ok()
