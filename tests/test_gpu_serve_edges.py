@@ -123,3 +123,31 @@ def test_append_reports_lengths_too_small_for_the_rows(lens, cu, skipped):
     # an idle sequence is no error
     s2.s2attn_rope_append(*args, _ints([3, 0]), cu_dev)
     _ok()
+
+
+@pytest.mark.parametrize("width", [2, 70])       # whole segments; the list form, which splits (70 x 16 tokens)
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (16, 1, 128)])
+def test_decode_bad_pages_count_as_zeros_and_lengths_are_cut(width, hq, hkv, d):
+    page, B = 16, 3
+    n = width * page - 3
+    pages = 3 * width
+    kc, vc = _randn(2, pages, page, hkv, d), _randn(3, pages, page, hkv, d)
+    q = _randn(1, B, hq, d)
+    good = [list(range(b * width, (b + 1) * width)) for b in range(B)]
+
+    def reference(table, lens):
+        """Tokens of a bad page: keys and values of zeros, in two more pages behind the cache's own."""
+        k0, v0 = (torch.cat((x, torch.zeros(1, page, hkv, d, dtype=x.dtype, device="cuda"))) for x in (kc, vc))
+        rows = [[x if 0 <= x < pages else pages for x in r] for r in table]
+        return k0, v0, rows, [min(max(m, 0), width * page) for m in lens]
+
+    for bad, lens, site in ((pages, [n, n, n], 0x80), (-1, [n, n, n], 0x80), (1 << 30, [n, 5, n], 0x80),
+                            (None, [n, width * page + 1, 7], 0x81), (None, [n, -1, (1 << 31) - 1], 0x81)):
+        table = [list(r) for r in good]
+        if bad is not None:
+            table[1][0] = table[2][width - 1] = bad
+        o, lse = s2.decode(q, kc, vc, _ints(table), _ints(lens))
+        torch.cuda.synchronize()
+        assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (7 << 8) | site)
+        k0, v0, rows, cut = reference(table, lens)
+        _check_decode(q, k0, v0, rows, cut, d ** -0.5, o, lse)
