@@ -82,6 +82,7 @@ cudaError_t set_smem_attrs() {
 namespace s2host {
 
 s2attn_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();   // told here: the next call's own check must not find it again
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, cudaGetErrorString(e));
   return S2ATTN_ERR_CUDA;
 }

@@ -151,3 +151,32 @@ def test_decode_bad_pages_count_as_zeros_and_lengths_are_cut(width, hq, hkv, d):
         assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (7 << 8) | site)
         k0, v0, rows, cut = reference(table, lens)
         _check_decode(q, k0, v0, rows, cut, d ** -0.5, o, lse)
+
+
+# ------------------------------------------------------------------------------------------
+# a failed launch
+# ------------------------------------------------------------------------------------------
+def test_a_failed_launch_is_not_the_next_call_s_error():
+    """A launch into a stream whose capture has been broken off fails on the host, before anything reaches the
+    GPU. The call that failed says so; the calls after it are not told again."""
+    rt = ctypes.CDLL("libcudart.so.12")                # the runtime that torch has loaded
+    side = torch.cuda.Stream()
+    handle = ctypes.c_void_p(side.cuda_stream)
+    q = _randn(1, 64, 2, 64).unsqueeze(0)
+    p = q[0]
+    want = s2.fwd(q, q, q, 64)
+    o, lse = torch.empty_like(p), torch.empty(2, 64, device="cuda")
+    s2.s2attn_prompt_fwd(p, p, p, o, lse, [0, 64])
+    torch.cuda.synchronize()
+    graph = ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(handle, 1) == 0                      # thread-local mode
+    try:
+        assert rt.cudaStreamSynchronize(handle) != 0                      # breaks the capture off
+        with pytest.raises(s2.S2AttnError, match="launch"):
+            s2.s2attn_prompt_fwd(p, p, p, o, lse, [0, 64], stream=side)
+    finally:
+        rt.cudaStreamEndCapture(handle, ctypes.byref(graph))
+        rt.cudaGetLastError()
+    got = s2.fwd(q, q, q, 64)
+    _ok()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
