@@ -88,6 +88,8 @@ s2attn_status check_heads(int Hq, int Hkv, int d) {
   return S2ATTN_OK;
 }
 
+bool too_many_rows(int B, int Hq) { return static_cast<long long>(B) * Hq >= (1ll << 31); }
+
 // A token (or batch row) stride: whole 16-byte chunks, rows that do not overlap.
 bool bad_row_stride(long long st, int heads, int d) {
   return st % 8 != 0 || st < static_cast<long long>(heads) * d;
@@ -300,7 +302,7 @@ s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void
 }
 
 size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
-  if (B <= 0 || check_heads(Hq, Hkv, d) != S2ATTN_OK) return 0;
+  if (B <= 0 || check_heads(Hq, Hkv, d) != S2ATTN_OK || too_many_rows(B, Hq)) return 0;
   const DecodeSpace w = decode_space(Hq / Hkv, d);
   return w.first + w.part + w.ml + w.tail;
 }
@@ -319,7 +321,7 @@ s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_ca
   if (B <= 0 || !(scale > 0.f) || !std::isfinite(scale)) return S2ATTN_ERR_INVALID_ARG;
   s2attn_status s = check_heads(Hq, Hkv, d);
   if (s != S2ATTN_OK) return s;
-  if (static_cast<long long>(B) * Hq >= (1ll << 31)) return S2ATTN_ERR_UNSUPPORTED;
+  if (too_many_rows(B, Hq)) return S2ATTN_ERR_UNSUPPORTED;
   s2::DecodeParams p{};
   if ((s = check_cache(Hkv, d, pages, page_size, max_pages, strides ? strides + 2 : nullptr, p.kc,
                        p.vc)) != S2ATTN_OK)

@@ -1,0 +1,19 @@
+"""CPU-side checks of the serving entries' Python face and of what the library answers without a GPU."""
+import pytest
+import torch
+
+import shifted_sparse_attention_fwd_b200 as s2
+from shifted_sparse_attention_fwd_b200 import build as s2build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    s2build.build()
+    return s2.lib()
+
+
+def test_decode_workspace_is_0_for_every_call_that_decode_rejects(lib):
+    """Also for batches of 2^31 rows and more, which s2attn_decode has no room to number."""
+    f = lib.s2attn_decode_workspace_size
+    assert f(1 << 29, 4, 2, 64) == 0 and f((1 << 31) - 1, 2, 2, 128) == 0
+    assert f((1 << 29) - 1, 4, 2, 64) == f(1, 4, 2, 64) > 0
