@@ -381,7 +381,9 @@ S2ATTN_API s2attn_status s2attn_rope_pi(const void* x, void* y, int B, int N, in
  * NULL (T = B: one new token each). cache_lens[s] counts the sequence's tokens INCLUDING these, so
  * row i of its n new rows has position cache_lens[s] - n + i. Queries and keys turn by the angle
  * of that position, pair (x[i], x[i + d/2]) by position * pi_scale * base^(-2i/d) (as
- * s2attn_rope_pi, but exact to fp32 rounding of sine and cosine at any position); turned queries
+ * s2attn_rope_pi, but with the angle exact to fp32 rounding of sine and cosine at any position, for
+ * base and pi_scale as they are passed: _f64 takes those that fp32 does not hold, such as 0.3, whose
+ * fp32 neighbour's angle is off by 1.6e-3 rad at position 131071); turned queries
  * go to q_rot, turned keys to the cache and, if not NULL, to k_rot, values to the cache.
  * q_rot may be q, k_rot may be k; no other overlap. q and q_rot may both be NULL. Rows behind
  * the last sequence, rows before the first and rows of an idle sequence (cache_lens = 0) are
@@ -400,6 +402,13 @@ S2ATTN_API s2attn_status s2attn_rope_append(const void* q, void* q_rot, const vo
                                             int d, int pages, int page_size, int max_pages,
                                             float base, float pi_scale, const long long* strides,
                                             void* stream);
+S2ATTN_API s2attn_status s2attn_rope_append_f64(const void* q, void* q_rot, const void* k, void* k_rot,
+                                                const void* v, void* k_cache, void* v_cache,
+                                                const int* block_table, const int* cu_seqlens,
+                                                const int* cache_lens, int T, int B, int Hq, int Hkv,
+                                                int d, int pages, int page_size, int max_pages,
+                                                double base, double pi_scale,
+                                                const long long* strides, void* stream);
 
 /* Device workspace of s2attn_decode (256-byte aligned; contents on entry do not matter): about 12
  * MB at d = 128 and 16 or more query heads per kv head, proportional to the smaller of that

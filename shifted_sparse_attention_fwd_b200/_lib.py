@@ -29,6 +29,7 @@ S2ATTN_FLAG_PARTIAL_LAST_GROUP = 4
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _Z = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/s2attn.h
@@ -57,6 +58,7 @@ SIGNATURES = {
     "s2attn_bwd_dq_ds_general": (_I, [_P] * 2 + [_I] * 6 + [_F, _I, _I, _I, _P, _P, _Z, _P]),
     "s2attn_get_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint)]),
     "s2attn_rope_append": (_I, [_P] * 10 + [_I] * 8 + [_F, _F, _P, _P]),
+    "s2attn_rope_append_f64": (_I, [_P] * 10 + [_I] * 8 + [_D, _D, _P, _P]),
     "s2attn_decode_workspace_size": (_Z, [_I] * 4),
     "s2attn_decode": (_I, [_P] * 7 + [_I] * 7 + [_F, _P, _P, _Z, _P]),
     "s2attn_prompt_fwd": (_I, [_P] * 6 + [_I] * 5 + [_F, _P, _P]),

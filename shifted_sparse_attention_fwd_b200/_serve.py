@@ -34,7 +34,7 @@ def _load():
                            f"{torch.__version__}: build it again")
     handle = lib()
     _s2torch.bind(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
-        "s2attn_rope_append", "s2attn_decode", "s2attn_decode_workspace_size", "s2attn_prompt_fwd")))
+        "s2attn_rope_append_f64", "s2attn_decode", "s2attn_decode_workspace_size", "s2attn_prompt_fwd")))
     _binding = _s2torch
     return _s2torch
 
@@ -49,7 +49,8 @@ def s2attn_rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cac
     into the paged cache (and k_rot unless None; may be k), and copy v [T,Hkv,d] into the cache.
     k_cache, v_cache [pages,page_size,Hkv,d]; block_table int32 [B,max_pages]; cache_lens int32 [B],
     the tokens of each sequence including the new ones; cu_seqlens int32 [B+1], the sequences' first
-    rows, or None for one new token per sequence. A bad page or length on the device is reported by
+    rows, or None for one new token per sequence. base and pi_scale are taken as Python floats, in 64 bits
+    (the library's s2attn_rope_append_f64). A bad page or length on the device is reported by
     s2attn_get_device_error."""
     status = (_binding or _load()).rope_append(
         False, q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, base, pi_scale,

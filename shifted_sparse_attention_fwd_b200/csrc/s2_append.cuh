@@ -5,9 +5,9 @@
 //
 // For position t and i < D/2 the pair (x[i], x[i + D/2]) turns by t * pi_scale * base^(-2i/D).
 // Positions reach 10^5 and more, where an fp32 product is off by 1e-2 rad; the angle is instead
-// formed in turns, as 64-bit fixed point: F_i = frac(pi_scale * base^(-2i/D) / 2 pi) * 2^64 (from
-// the host, rounded once), and t * F_i modulo 2^64 is the exact fraction of a turn (error
-// t * 2^-64). Its upper 32 bits, as a signed number, are sincospif's argument.
+// formed in turns, as 64-bit fixed point: F_i = frac(pi_scale * base^(-2i/D) / 2 pi) * 2^64 (on the
+// host, from base and pi_scale in 64 bits, rounded once), and t * F_i modulo 2^64 is the exact
+// fraction of a turn (error t * 2^-64). Its upper 32 bits, as a signed number, are sincospif's argument.
 //
 // Memory bound: every element is read once and written once or twice. A block takes a few tokens;
 // one lane per token finds its sequence (binary search of cu_seqlens) and slot, and all threads the

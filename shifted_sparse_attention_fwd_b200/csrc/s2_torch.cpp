@@ -24,7 +24,7 @@
 
 namespace {
 
-decltype(&s2attn_rope_append) g_append = nullptr;
+decltype(&s2attn_rope_append_f64) g_append = nullptr;
 decltype(&s2attn_decode) g_decode = nullptr;
 decltype(&s2attn_decode_workspace_size) g_decode_space = nullptr;
 decltype(&s2attn_prompt_fwd) g_prompt = nullptr;
@@ -228,7 +228,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const int*>(data(cu)), static_cast<const int*>(data(lens)), static_cast<int>(T),
         static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d),
         static_cast<int>(kc.size(0)), static_cast<int>(kc.size(1)), static_cast<int>(width),
-        static_cast<float>(base), static_cast<float>(pi), st, at_.stream);
+        base, pi, st, at_.stream);
     return fresh ? answer(status, q_rot, k_rot) : answer(status);
   });
 }

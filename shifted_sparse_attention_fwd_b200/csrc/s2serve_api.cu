@@ -126,8 +126,8 @@ s2::FastDiv fast_div_by(int d) {
 }
 
 // F_i of s2_append.cuh for one (base, pi_scale, d); the last one is kept by each host thread.
-const unsigned long long* turns(float base, float pi_scale, int d) {
-  static thread_local struct { float base, pi; int d; unsigned long long f[64]; } last = {0.f, 0.f, 0, {}};
+const unsigned long long* turns(double base, double pi_scale, int d) {
+  static thread_local struct { double base, pi; int d; unsigned long long f[64]; } last = {0.0, 0.0, 0, {}};
   if (last.base != base || last.pi != pi_scale || last.d != d) {
     const long double two_pi = 6.283185307179586476925286766559L;
     for (int i = 0; i < d / 2; ++i) {
@@ -251,23 +251,17 @@ s2attn_status launch_prompt(s2::PromptParams& p, const CUtensorMap (&maps)[4], c
   return S2ATTN_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void* k_rot,
-                                 const void* v, void* k_cache, void* v_cache,
-                                 const int* block_table, const int* cu_seqlens,
-                                 const int* cache_lens, int T, int B, int Hq, int Hkv, int d,
-                                 int pages, int page_size, int max_pages, float base,
-                                 float pi_scale, const long long* strides, void* stream) {
+s2attn_status rope_append(const void* q, void* q_rot, const void* k, void* k_rot, const void* v, void* k_cache,
+                          void* v_cache, const int* block_table, const int* cu_seqlens, const int* cache_lens, int T,
+                          int B, int Hq, int Hkv, int d, int pages, int page_size, int max_pages, double base,
+                          double pi_scale, const long long* strides, void* stream) {
   if (!k || !v || !k_cache || !v_cache || !block_table || !cache_lens) return S2ATTN_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_rot == nullptr)) return S2ATTN_ERR_INVALID_ARG;
   const void* ptrs[7] = {q, q_rot, k, k_rot, v, k_cache, v_cache};
   for (const void* x : ptrs)
     if (!aligned16(x)) return S2ATTN_ERR_INVALID_ARG;
   if (T <= 0 || B <= 0 || (!cu_seqlens && T != B)) return S2ATTN_ERR_INVALID_ARG;
-  if (!(base > 1.f) || !std::isfinite(base) || !(pi_scale > 0.f) || !std::isfinite(pi_scale))
+  if (!(base > 1.0) || !std::isfinite(base) || !(pi_scale > 0.0) || !std::isfinite(pi_scale))
     return S2ATTN_ERR_INVALID_ARG;
   s2attn_status s = check_heads(Hq, Hkv, d);
   if (s != S2ATTN_OK) return s;
@@ -299,6 +293,30 @@ s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void
   if ((s = serve_device(&p.err, &num_sms)) != S2ATTN_OK) return s;
   cudaStream_t sm = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_append<64>(p, num_sms, sm) : launch_append<128>(p, num_sms, sm);
+}
+
+}  // namespace
+
+extern "C" {
+
+s2attn_status s2attn_rope_append(const void* q, void* q_rot, const void* k, void* k_rot,
+                                 const void* v, void* k_cache, void* v_cache,
+                                 const int* block_table, const int* cu_seqlens,
+                                 const int* cache_lens, int T, int B, int Hq, int Hkv, int d,
+                                 int pages, int page_size, int max_pages, float base,
+                                 float pi_scale, const long long* strides, void* stream) {
+  return rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cu_seqlens, cache_lens, T, B, Hq, Hkv, d,
+                     pages, page_size, max_pages, base, pi_scale, strides, stream);
+}
+
+s2attn_status s2attn_rope_append_f64(const void* q, void* q_rot, const void* k, void* k_rot,
+                                     const void* v, void* k_cache, void* v_cache,
+                                     const int* block_table, const int* cu_seqlens,
+                                     const int* cache_lens, int T, int B, int Hq, int Hkv, int d,
+                                     int pages, int page_size, int max_pages, double base,
+                                     double pi_scale, const long long* strides, void* stream) {
+  return rope_append(q, q_rot, k, k_rot, v, k_cache, v_cache, block_table, cu_seqlens, cache_lens, T, B, Hq, Hkv, d,
+                     pages, page_size, max_pages, base, pi_scale, strides, stream);
 }
 
 size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {

@@ -154,6 +154,25 @@ def test_decode_bad_pages_count_as_zeros_and_lengths_are_cut(width, hq, hkv, d):
 
 
 # ------------------------------------------------------------------------------------------
+# scales that fp32 does not hold
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("base,pi", [(10000.0, 0.3), (10000.0, 4096 / 100000), (500000.7, 1 / 3), (1e6, 0.1)])
+def test_append_angles_of_any_scale_at_far_positions(base, pi):
+    """base and pi_scale are Python floats; the angle is that of their product, not of its fp32 neighbour
+    (0.3 in fp32 is off by 1.6e-3 rad at position 131071)."""
+    hq, hkv, d, page = 2, 1, 128, 1 << 12
+    pos = [131071, 131072 - 4096, 99999, 65537, 1, 0]
+    k, q, v = (_randn(7 + i, len(pos), h, d) for i, h in enumerate((hkv, hq, hkv)))
+    kc, vc = _randn(1, len(pos), page, hkv, d), _randn(2, len(pos), page, hkv, d)
+    table = _ints([[b] * 32 for b in range(len(pos))])
+    q_rot, k_rot = s2.rope_append(q, k, v, kc, vc, table, _ints([p + 1 for p in pos]), base=base, pi_scale=pi)
+    _ok()
+    at = torch.tensor(pos, device="cuda")
+    _near_bf16(q_rot, _turn64(q, at, base, pi), 1.2e-5)
+    _near_bf16(k_rot, _turn64(k, at, base, pi), 1.2e-5)
+
+
+# ------------------------------------------------------------------------------------------
 # a failed launch
 # ------------------------------------------------------------------------------------------
 def test_a_failed_launch_is_not_the_next_call_s_error():

@@ -17,3 +17,14 @@ def test_decode_workspace_is_0_for_every_call_that_decode_rejects(lib):
     f = lib.s2attn_decode_workspace_size
     assert f(1 << 29, 4, 2, 64) == 0 and f((1 << 31) - 1, 2, 2, 128) == 0
     assert f((1 << 29) - 1, 4, 2, 64) == f(1, 4, 2, 64) > 0
+
+
+def _append_f64(lib, base, pi):
+    A = 0x10000   # fake device address: never dereferenced
+    return lib.s2attn_rope_append_f64(*[A] * 10, 9, 3, 4, 2, 64, 5, 16, 2, base, pi, None, None)
+
+
+@pytest.mark.parametrize("base,pi", [(1.0, 0.5), (float("inf"), 0.5), (float("nan"), 0.5), (1e4, 0.0), (1e4, -0.3),
+                                     (1e4, float("nan")), (1e4, float("inf"))])
+def test_append_f64_rejects(lib, base, pi):
+    assert _append_f64(lib, base, pi) == s2.S2ATTN_ERR_INVALID_ARG
