@@ -5,7 +5,8 @@ The checks of a call's tensors, its allocations and the call itself are in _s2to
 (csrc/s2_torch.cpp), a few microseconds less than they take here; there is no other path. Wrong tensors
 raise ValueError, a failed call S2AttnError. Tensors on another device than the current one run there, on
 that device's current stream; `stream` (a torch.cuda.Stream or a handle) overrides it. Views with
-contiguous (heads, d) blocks are accepted wherever a tensor of heads is.
+contiguous (heads, d) blocks are accepted wherever a tensor of heads is. A call of no rows (a scheduler's
+empty step: no new tokens, no sequences to decode) launches nothing and returns empty tensors.
 """
 from __future__ import annotations
 

@@ -15,6 +15,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <climits>
+#include <cmath>
 #include <initializer_list>
 #include <optional>
 #include <stdexcept>
@@ -144,6 +146,14 @@ double number(PyObject* o) {
   return x;
 }
 
+// A call of no rows has nothing to launch (the library takes at least one); its other arguments are checked as
+// the library checks them.
+int check_heads(int64_t Hq, int64_t Hkv, int64_t d) {
+  if (Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return S2ATTN_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? S2ATTN_OK : S2ATTN_ERR_UNSUPPORTED;
+}
+bool positive(double x) { return x > 0.0 && std::isfinite(x); }
+
 void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // What each function returns: the status if it is not OK, else the new tensors or None.
@@ -223,6 +233,11 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (q.defined()) q_rot = empty({T, Hq, d}, at::kBFloat16, dev);
       k_rot = empty({T, Hkv, d}, at::kBFloat16, dev);
     }
+    if (T == 0) {   // of as many sequences as there are, if none of them has new rows
+      int status = check_heads(Hq, Hkv, d);
+      if ((!cu.defined() && B != 0) || !positive(base - 1.0) || !positive(pi)) status = S2ATTN_ERR_INVALID_ARG;
+      return fresh ? answer(status, q_rot, k_rot) : answer(status);
+    }
     const int status = g_append(
         data(q), data(q_rot), data(k), data(k_rot), data(v), data(kc), data(vc), static_cast<const int*>(data(table)),
         static_cast<const int*>(data(cu)), static_cast<const int*>(data(lens)), static_cast<int>(T),
@@ -262,6 +277,10 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (fresh) {
       o = empty({B, Hq, d}, at::kBFloat16, dev);
       lse = empty({B, Hq}, at::kFloat, dev);
+    }
+    if (B == 0) {
+      const int status = positive(static_cast<float>(scale)) ? check_heads(Hq, Hkv, d) : S2ATTN_ERR_INVALID_ARG;
+      return fresh ? answer(status, o, lse) : answer(status);
     }
     if (!space.defined())
       space = empty({static_cast<int64_t>(g_decode_space(static_cast<int>(B), static_cast<int>(Hq),
@@ -304,6 +323,13 @@ PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (fresh) {
       o = empty({T, Hq, d}, at::kBFloat16, dev);
       lse = empty({Hq, T}, at::kFloat, dev);
+    }
+    if (T == 0) {   // sequences of no rows
+      int status = positive(static_cast<float>(scale)) ? check_heads(Hq, Hkv, d) : S2ATTN_ERR_INVALID_ARG;
+      if (cu.numel() == 0) status = S2ATTN_ERR_INVALID_ARG;
+      for (int64_t i = 0; i < cu.numel(); ++i)
+        if (cu.const_data_ptr<int>()[i] != 0) status = S2ATTN_ERR_INVALID_ARG;
+      return fresh ? answer(status, o, lse) : answer(status);
     }
     const int status =
         g_prompt(data(q), data(k), data(v), data(o), static_cast<float*>(data(lse)), static_cast<const int*>(data(cu)),

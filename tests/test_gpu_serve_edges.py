@@ -173,6 +173,49 @@ def test_append_angles_of_any_scale_at_far_positions(base, pi):
 
 
 # ------------------------------------------------------------------------------------------
+# empty calls
+# ------------------------------------------------------------------------------------------
+def test_empty_calls_return_empty_tensors():
+    """A scheduler's empty step: no new rows, no sequences. Nothing is launched or written."""
+    hq, hkv, d, page = 8, 2, 64, 16
+    kc, vc = _randn(1, 3, page, hkv, d), _randn(2, 3, page, hkv, d)
+    kc0, vc0 = kc.clone(), vc.clone()
+    q, k = _randn(3, 0, hq, d), _randn(4, 0, hkv, d)
+    none = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    some, lens = _ints([[0, 1], [2, 2]]), _ints([5, 0])
+    for table, n, cu in ((none, _ints([]), None), (none, _ints([]), _ints([0])), (some, lens, _ints([0, 0, 0]))):
+        q_rot, k_rot = s2.rope_append(q, k, k, kc, vc, table, n, cu)
+        assert q_rot.shape == q.shape and k_rot.shape == k.shape and q_rot.dtype == torch.bfloat16
+        q_rot, k_rot = s2.rope_append(None, k, k, kc, vc, table, n, cu)
+        assert q_rot is None and k_rot.shape == k.shape
+        s2.s2attn_rope_append(q, q, k, None, k, kc, vc, table, n, cu)
+    o, lse = s2.decode(q, kc, vc, none, _ints([]))
+    assert o.shape == (0, hq, d) and lse.shape == (0, hq) and lse.dtype == torch.float32
+    s2.s2attn_decode(q, kc, vc, none, _ints([]), o, None)
+    for cu in ([0], [0, 0], torch.zeros(4, dtype=torch.int32)):
+        o, lse = s2.prompt_fwd(q, k, k, cu)
+        assert o.shape == q.shape and lse.shape == (hq, 0)
+        s2.s2attn_prompt_fwd(q, k, k, o, lse, cu)
+    _ok()
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+    # what is wrong in a call of some rows is wrong in one of none
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.rope_append(q, k, k, kc, vc, some, lens)                       # T != B and no cu_seqlens
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.prompt_fwd(q, k, k, [0, 1])
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.prompt_fwd(q, k, k, [])
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.decode(_randn(1, 0, 3, d), kc, vc, none, _ints([]))            # 3 query heads over 2
+    with pytest.raises(s2.S2AttnError, match="unsupported"):
+        s2.prompt_fwd(_randn(1, 0, 4, 96), _randn(1, 0, 2, 96), _randn(1, 0, 2, 96), [0])
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.decode(q, kc, vc, none, _ints([]), scale=-1.0)
+    with pytest.raises(s2.S2AttnError, match="invalid"):
+        s2.rope_append(q, k, k, kc, vc, none, _ints([]), pi_scale=0.0)
+
+
+# ------------------------------------------------------------------------------------------
 # a failed launch
 # ------------------------------------------------------------------------------------------
 def test_a_failed_launch_is_not_the_next_call_s_error():
