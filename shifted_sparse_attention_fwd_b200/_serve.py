@@ -6,7 +6,8 @@ The checks of a call's tensors, its allocations and the call itself are in _s2to
 raise ValueError, a failed call S2AttnError. Tensors on another device than the current one run there, on
 that device's current stream; `stream` (a torch.cuda.Stream or a handle) overrides it. Views with
 contiguous (heads, d) blocks are accepted wherever a tensor of heads is. A call of no rows (a scheduler's
-empty step: no new tokens, no sequences to decode) launches nothing and returns empty tensors.
+empty step: no new tokens, no sequences to decode) launches nothing and returns empty tensors. There is no
+backward: tensors that require grad are refused unless under torch.no_grad or inference_mode.
 """
 from __future__ import annotations
 

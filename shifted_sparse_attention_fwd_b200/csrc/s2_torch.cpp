@@ -10,6 +10,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -21,6 +23,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/s2attn.h"
 
@@ -76,6 +79,19 @@ void check(const Tensor& t, const char* name, at::ScalarType type, Sizes shape, 
 void check_packed(const Tensor& t, const char* name, at::ScalarType type, Sizes shape, int device) {
   check(t, name, type, shape, device);
   if (!t.is_contiguous()) refuse(name, "expected a contiguous tensor");
+}
+
+// There is no backward. A graph that would end here is refused rather than cut in silence: a tensor that
+// requires grad while gradients are recorded, or that carries a forward-mode tangent.
+void refuse_gradients(std::initializer_list<std::pair<const Tensor*, const char*>> tensors) {
+  for (const auto& [t, name] : tensors) {
+    // (a tensor without autograd data, as in serving, has neither)
+    if (!t->defined() || t->unsafeGetTensorImpl()->autograd_meta() == nullptr) continue;
+    if (c10::GradMode::is_enabled() && t->requires_grad())
+      refuse(name, "requires grad, and the serving entries have no backward (call them under torch.no_grad())");
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t->_fw_grad(0).defined())
+      refuse(name, "has a forward-mode tangent, and the serving entries have no derivative");
+  }
 }
 
 // Shape of the tensor that gives a call its sizes.
@@ -227,6 +243,8 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_packed(table, "block_table", at::kInt, {B, width}, dev);
     check_packed(lens, "cache_lens", at::kInt, {B}, dev);
     if (cu.defined()) check_packed(cu, "cu_seqlens", at::kInt, {B + 1}, dev);
+    refuse_gradients({{&q, "q"}, {&q_rot, "q_rot"}, {&k, "k"}, {&k_rot, "k_rot"}, {&v, "v"}, {&kc, "k_cache"},
+                      {&vc, "v_cache"}});
     const double base = number(a[11]), pi = number(a[12]);
     const Place at_(dev, a[13]);
     if (fresh) {
@@ -272,6 +290,7 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_packed(lens, "cache_lens", at::kInt, {B}, dev);
     if (lse.defined()) check_packed(lse, "lse", at::kFloat, {B, Hq}, dev);
     if (space.defined()) check_packed(space, "workspace", at::kByte, {space.numel()}, dev);
+    refuse_gradients({{&q, "q"}, {&kc, "k_cache"}, {&vc, "v_cache"}, {&o, "o"}, {&lse, "lse"}});
     const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[8]);
     const Place at_(dev, a[10]);
     if (fresh) {
@@ -318,6 +337,7 @@ PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (cu.is_cuda() || cu.scalar_type() != at::kInt || cu.dim() != 1 || !cu.is_contiguous())
       refuse("cu_seqlens", "expected a contiguous int32 CPU tensor of one axis, or a sequence of ints");
+    refuse_gradients({{&q, "q"}, {&k, "k"}, {&v, "v"}, {&o, "o"}, {&lse, "lse"}});
     const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[7]);
     const Place at_(dev, a[8]);
     if (fresh) {

@@ -216,6 +216,46 @@ def test_empty_calls_return_empty_tensors():
 
 
 # ------------------------------------------------------------------------------------------
+# autograd
+# ------------------------------------------------------------------------------------------
+def _small():
+    hq, hkv, d, page = 4, 2, 64, 8
+    t = dict(q=_randn(1, 2, hq, d), k=_randn(2, 2, hkv, d), v=_randn(3, 2, hkv, d),
+             k_cache=_randn(4, 3, page, hkv, d), v_cache=_randn(5, 3, page, hkv, d))
+    return t, _ints([[0], [2]]), _ints([3, 8])
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "k_cache", "v_cache"])
+def test_tensors_that_need_a_gradient_are_refused(name):
+    """There is no backward: a graph that would end at the call is refused, not cut in silence. Under
+    torch.no_grad the same tensors are fine, and give the same result."""
+    t, table, lens = _small()
+    plain = {n: x.clone() for n, x in t.items()}
+    t[name].requires_grad_()
+
+    def calls(t):
+        yield "append", lambda: s2.rope_append(t["q"], t["k"], t["v"], t["k_cache"], t["v_cache"], table, lens)
+        yield "decode", lambda: s2.decode(t["q"], t["k_cache"], t["v_cache"], table, lens)
+        yield "prompt", lambda: s2.prompt_fwd(t["q"], t["k"], t["v"], [0, 2])
+    uses = {"append": ("q", "k", "v", "k_cache", "v_cache"), "decode": ("q", "k_cache", "v_cache"),
+            "prompt": ("q", "k", "v")}
+    for (op, call), (_, want) in zip(calls(t), calls(plain)):
+        if name in uses[op]:
+            with pytest.raises(ValueError, match=f"{name}: requires grad"):
+                call()
+        with torch.no_grad():
+            for x, y in zip(call(), want()):
+                assert torch.equal(x, y) and not x.requires_grad
+        with torch.inference_mode():
+            call()
+    _ok()
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(plain["q"], torch.ones_like(plain["q"]))
+        with pytest.raises(ValueError, match="q: .*tangent"):
+            s2.decode(dual, plain["k_cache"], plain["v_cache"], table, lens)
+
+
+# ------------------------------------------------------------------------------------------
 # a failed launch
 # ------------------------------------------------------------------------------------------
 def test_a_failed_launch_is_not_the_next_call_s_error():
