@@ -94,6 +94,14 @@ void refuse_gradients(std::initializer_list<std::pair<const Tensor*, const char*
   }
 }
 
+// What a call writes in place counts as changed, for a graph that holds it (tensors of inference mode keep no count).
+int written(int status, std::initializer_list<const Tensor*> tensors) {
+  if (status != S2ATTN_OK) return status;
+  for (const Tensor* t : tensors)
+    if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  return status;
+}
+
 // Shape of the tensor that gives a call its sizes.
 void want_axes(const Tensor& t, const char* name, int64_t n) {
   if (t.dim() != n) refuse(name, "expected " + std::to_string(n) + " axes, got " + std::to_string(t.dim()));
@@ -256,12 +264,13 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if ((!cu.defined() && B != 0) || !positive(base - 1.0) || !positive(pi)) status = S2ATTN_ERR_INVALID_ARG;
       return fresh ? answer(status, q_rot, k_rot) : answer(status);
     }
-    const int status = g_append(
+    int status = g_append(
         data(q), data(q_rot), data(k), data(k_rot), data(v), data(kc), data(vc), static_cast<const int*>(data(table)),
         static_cast<const int*>(data(cu)), static_cast<const int*>(data(lens)), static_cast<int>(T),
         static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d),
         static_cast<int>(kc.size(0)), static_cast<int>(kc.size(1)), static_cast<int>(width),
         base, pi, st, at_.stream);
+    status = fresh ? written(status, {&kc, &vc}) : written(status, {&q_rot, &k_rot, &kc, &vc});
     return fresh ? answer(status, q_rot, k_rot) : answer(status);
   });
 }
@@ -305,12 +314,13 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       space = empty({static_cast<int64_t>(g_decode_space(static_cast<int>(B), static_cast<int>(Hq),
                                                          static_cast<int>(Hkv), static_cast<int>(d)))},
                     at::kByte, dev);
-    const int status =
+    int status =
         g_decode(data(q), data(kc), data(vc), static_cast<const int*>(data(table)),
                  static_cast<const int*>(data(lens)), data(o), static_cast<float*>(data(lse)), static_cast<int>(B),
                  static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), static_cast<int>(kc.size(0)),
                  static_cast<int>(kc.size(1)), static_cast<int>(width), static_cast<float>(scale), st, data(space),
                  static_cast<size_t>(space.numel()), at_.stream);
+    if (!fresh) status = written(status, {&o, &lse});
     return fresh ? answer(status, o, lse) : answer(status);
   });
 }
@@ -351,10 +361,11 @@ PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (cu.const_data_ptr<int>()[i] != 0) status = S2ATTN_ERR_INVALID_ARG;
       return fresh ? answer(status, o, lse) : answer(status);
     }
-    const int status =
+    int status =
         g_prompt(data(q), data(k), data(v), data(o), static_cast<float*>(data(lse)), static_cast<const int*>(data(cu)),
                  static_cast<int>(cu.numel()) - 1, static_cast<int>(T), static_cast<int>(Hq), static_cast<int>(Hkv),
                  static_cast<int>(d), static_cast<float>(scale), st, at_.stream);
+    if (!fresh) status = written(status, {&o, &lse});
     return fresh ? answer(status, o, lse) : answer(status);
   });
 }

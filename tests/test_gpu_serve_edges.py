@@ -255,6 +255,39 @@ def test_tensors_that_need_a_gradient_are_refused(name):
             s2.decode(dual, plain["k_cache"], plain["v_cache"], table, lens)
 
 
+def test_writes_raise_the_version_of_what_they_write():
+    """Autograd's check for tensors changed in place sees the caches and the outputs that a call is given; what
+    it only reads keeps its version. Tensors of inference mode, which have none, can be written."""
+    t, table, lens = _small()
+    q, k, v, kc, vc = t.values()
+    o, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+    plse = torch.empty(4, 2, device="cuda")
+
+    def versions():
+        return [x._version for x in (q, k, v, kc, vc, o, lse, plse, table, lens)]
+    a = versions()
+    s2.rope_append(q, k, v, kc, vc, table, lens)
+    b = versions()
+    assert [y - x for x, y in zip(a, b)] == [0, 0, 0, 1, 1, 0, 0, 0, 0, 0]
+    s2.s2attn_rope_append(q, q, k, k, v, kc, vc, table, lens)
+    c = versions()
+    assert [y - x for x, y in zip(b, c)] == [1, 1, 0, 1, 1, 0, 0, 0, 0, 0]
+    s2.s2attn_decode(q, kc, vc, table, lens, o, lse)
+    d = versions()
+    assert [y - x for x, y in zip(c, d)] == [0, 0, 0, 0, 0, 1, 1, 0, 0, 0]
+    s2.s2attn_prompt_fwd(q, k, v, o, plse, [0, 2])
+    assert [y - x for x, y in zip(d, versions())] == [0, 0, 0, 0, 0, 1, 0, 1, 0, 0]
+    half = torch.ones(1, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = (half * kc).sum()                              # a graph that holds the cache
+    s2.rope_append(q, k, v, kc, vc, table, lens)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        ki, vi = kc.clone(), vc.clone()
+    s2.rope_append(q, k, v, ki, vi, table, lens)
+    _ok()
+
+
 # ------------------------------------------------------------------------------------------
 # a failed launch
 # ------------------------------------------------------------------------------------------
