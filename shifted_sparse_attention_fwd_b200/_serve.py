@@ -82,7 +82,7 @@ def s2attn_decode(q, k_cache, v_cache, block_table, cache_lens, o, lse, scale=No
 def _host_ints(cu_seqlens):
     if isinstance(cu_seqlens, torch.Tensor):
         return cu_seqlens
-    return torch.tensor(cu_seqlens, dtype=torch.int32)
+    return torch.tensor(cu_seqlens, dtype=torch.int32, device="cpu")   # (whatever torch's default device is)
 
 
 def s2attn_prompt_fwd(q, k, v, o, lse, cu_seqlens, scale=None, stream=None):

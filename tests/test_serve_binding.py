@@ -28,3 +28,11 @@ def _append_f64(lib, base, pi):
                                      (1e4, float("nan")), (1e4, float("inf"))])
 def test_append_f64_rejects(lib, base, pi):
     assert _append_f64(lib, base, pi) == s2.S2ATTN_ERR_INVALID_ARG
+
+
+def test_lengths_given_as_ints_stay_on_the_host():
+    """prompt_fwd takes a list of ints under any default device of torch's."""
+    from shifted_sparse_attention_fwd_b200 import _serve
+    with torch.device("meta"):
+        cu = _serve._host_ints([0, 5, 9])
+    assert cu.device.type == "cpu" and cu.dtype == torch.int32 and cu.tolist() == [0, 5, 9]
