@@ -17,6 +17,7 @@ SRCS = [os.path.join(PKG_DIR, "csrc", f) for f in ("s2attn_api.cu", "s2serve_api
 LIB = os.path.join(PKG_DIR, "libs2attn.so")
 BINDING_SRC = os.path.join(PKG_DIR, "csrc", "s2_torch.cpp")
 BINDING = os.path.join(PKG_DIR, "_s2torch.so")
+BINDING_TORCH = os.path.join(PKG_DIR, "_build", "s2torch.version")   # the torch that it was built for
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -51,9 +52,19 @@ def _compile(cmd, out, verbose):
     os.replace(out + ".tmp", out)
 
 
-def build_binding(verbose: bool = False, force: bool = False) -> str:
+def binding_up_to_date() -> bool:
+    """Newer than its sources, and built for the torch that is installed."""
+    import torch
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_TORCH):
+        return False
+    with open(BINDING_TORCH) as f:
+        built_for = f.read().strip()
     newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(ROOT, "include", "s2attn.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    return built_for == torch.__version__ and os.path.getmtime(BINDING) >= newest
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    if not force and binding_up_to_date():
         return BINDING
     import torch
     torch_dir = os.path.dirname(torch.__file__)
@@ -65,6 +76,10 @@ def build_binding(verbose: bool = False, force: bool = False) -> str:
               "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, BINDING_SRC,
               "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
               "-ltorch_python", "-o", BINDING + ".tmp"], BINDING, verbose)
+    os.makedirs(os.path.dirname(BINDING_TORCH), exist_ok=True)
+    with open(BINDING_TORCH + ".tmp", "w") as f:
+        f.write(torch.__version__)
+    os.replace(BINDING_TORCH + ".tmp", BINDING_TORCH)
     return BINDING
 
 

@@ -36,3 +36,28 @@ def test_lengths_given_as_ints_stay_on_the_host():
     with torch.device("meta"):
         cu = _serve._host_ints([0, 5, 9])
     assert cu.device.type == "cpu" and cu.dtype == torch.int32 and cu.tolist() == [0, 5, 9]
+
+
+def test_build_makes_the_binding_again_for_another_torch(lib, monkeypatch, tmp_path):
+    """The binding fits one torch only and refuses to load with another, so build() follows the torch that is
+    installed, not the files' times alone."""
+    import os
+    compiled = []
+
+    def compile_(cmd, out, verbose):
+        compiled.append(out)
+        with open(out, "w"):
+            pass
+    monkeypatch.setattr(s2build, "_compile", compile_)
+    monkeypatch.setattr(s2build, "BINDING", str(tmp_path / "b.so"))
+    monkeypatch.setattr(s2build, "BINDING_TORCH", str(tmp_path / "x" / "version"), raising=False)
+    s2build.build_binding()
+    s2build.build_binding()
+    assert compiled == [str(tmp_path / "b.so")]
+    monkeypatch.setattr(torch, "__version__", "1.0.0+cu1")
+    s2build.build_binding()
+    s2build.build_binding()
+    assert len(compiled) == 2
+    os.remove(tmp_path / "b.so")
+    s2build.build_binding()
+    assert len(compiled) == 3
