@@ -420,8 +420,9 @@ S2ATTN_API size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
  * of sequence b (the new token's key and value among them, appended before), q, o bf16 [B, Hq, d],
  * lse fp32 [B, Hq] (natural log; may be NULL). Query head h reads kv head h / (Hq / Hkv); any
  * group size. q must be turned already. A sequence of length 0 gives o = 0 and lse = -inf.
- * Cache rows past a sequence's length are never used, whatever they hold. The same inputs give the
- * same bits. `strides`: NULL or {q, o batch strides, k_cache sp, st, v_cache sp, st}. Calls that
+ * Cache rows past a sequence's length are never used, whatever they hold; infinite values that are seen
+ * give infinite results. Finite values below 2^120 / cache_lens[b] never overflow the sums. The same inputs
+ * give the same bits. `strides`: NULL or {q, o batch strides, k_cache sp, st, v_cache sp, st}. Calls that
  * may run at the same time need a workspace each. Two launches (the second one joins what was
  * split), asynchronous on `stream`; allocates nothing.
  */
@@ -439,7 +440,9 @@ S2ATTN_API s2attn_status s2attn_decode(const void* q, const void* k_cache, const
  * call only). Row i of a sequence sees its rows 0..i: o = softmax(scale * q k^T) v, lse fp32 [Hq, T]
  * (natural log). Query head h reads kv head h / (Hq / Hkv); q and k must be turned already
  * (s2attn_rope_append with k_rot, s2attn_rope_pi). Rows of no sequence are neither read into a
- * result nor written, and what a row does not see never reaches it, NaN and infinities included.
+ * result nor written, and what a row does not see never reaches it, NaN and infinities included. Finite
+ * values must stay below 2^98 / ceil(n / 128) in a sequence of n rows: above, where a row's scores grow by
+ * 15 nats and more over its first 16, the sums may overflow although the result would not.
  * `strides`: NULL or the row strides of {q, k, v, o}, multiples of 8 and at least heads * d; tensors
  * must not overlap. T > 2^23 or Hq >= 2^20 -> S2ATTN_ERR_UNSUPPORTED. One launch per 512 sequences and
  * 2048 query tiles (of 128 rows, or 256 where Hq / Hkv is odd); a captured graph keeps the lengths it was

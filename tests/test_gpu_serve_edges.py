@@ -315,3 +315,41 @@ def test_a_failed_launch_is_not_the_next_call_s_error():
     got = s2.fwd(q, q, q, 64)
     _ok()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------------------------------
+# large values
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (3, 3, 64)])
+def test_prompt_values_up_to_the_stated_limit(hq, hkv, d):
+    """Values just below 2^98 / ceil(n / 128) under scores that grow to almost 2^30 in a tile's sum over a row's
+    first 16 (so the passes are not repeated): finite, and right."""
+    n = 500
+    q, k, v = (_randn(80 + i, n, h, d) for i, h in enumerate((hq, hkv, hkv)))
+    # the score of key r is 16 r / n nats: its weight over the first ones' 2^(23 r / n), a last tile's sum 2^28
+    q.fill_(1.0)
+    k.copy_((torch.arange(n, device="cuda") * (16.0 / n))[:, None, None].expand_as(k))
+    v.copy_((v.float().abs().clamp(0.5, 1.98) * 2.0 ** 95).to(torch.bfloat16))
+    cu = [0, n]
+    o, lse = s2.prompt_fwd(q, k, v, cu, scale=1.0 / d)
+    _ok()
+    want, want_lse, mean_abs = _prompt64(q, k, v, cu, 1.0 / d)
+    _near_bf16(o, want, (BF16_STEP + 1e-5) * mean_abs)
+    assert float((lse.double() - want_lse).abs().max()) <= 2e-5
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (12, 1, 64)])
+@pytest.mark.parametrize("n", [400, 1000])
+def test_decode_values_up_to_the_stated_limit(hq, hkv, d, n):
+    """Values just below 2^120 / n under scores that grow slowly, so that the sums keep a reference of up to 2^8
+    below them."""
+    page, lens = 16, [n, 1]
+    rows, pages = _table(lens, page, 4)
+    kc, vc = _randn(1, pages, page, hkv, d), _randn(2, pages, page, hkv, d)
+    q = torch.ones(2, hq, d, dtype=torch.bfloat16, device="cuda")
+    vc.copy_((vc.float().abs().clamp(0.5, 1.98) * 2.0 ** 109).to(torch.bfloat16))
+    t = torch.arange(n, device="cuda")
+    kc[torch.tensor(rows[0], device="cuda")[t // page], t % page] = (t * (16.0 / n))[:, None, None].to(torch.bfloat16)
+    o, lse = s2.decode(q, kc, vc, _ints(rows), _ints(lens), scale=1.0 / d)
+    _ok()
+    _check_decode(q, kc, vc, rows, lens, 1.0 / d, o, lse)
