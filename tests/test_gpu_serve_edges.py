@@ -353,3 +353,65 @@ def test_decode_values_up_to_the_stated_limit(hq, hkv, d, n):
     o, lse = s2.decode(q, kc, vc, _ints(rows), _ints(lens), scale=1.0 / d)
     _ok()
     _check_decode(q, kc, vc, rows, lens, 1.0 / d, o, lse)
+
+
+# ------------------------------------------------------------------------------------------
+# captured steps with other work between
+# ------------------------------------------------------------------------------------------
+def test_captured_steps_between_copies_fills_and_other_streams():
+    """The kernels may start before the work in front of them has ended, and wait for it: copies, fills, torch's
+    own kernels and a fork onto a second stream, captured and replayed, and queued without a capture."""
+    hq, hkv, d, page, B, width = 8, 2, 128, 16, 4, 40
+    kc, vc = _randn(1, B * width, page, hkv, d), _randn(2, B * width, page, hkv, d)
+    rows = [list(range(b * width, (b + 1) * width)) for b in range(B)]
+    table, lens = torch.zeros(B, width, dtype=torch.int32, device="cuda"), _ints([0] * B)
+    src = {"table": _ints(rows), "lens": _ints([599, 17, 0, 320]), "q": _randn(3, B, hq, d), "k": _randn(4, B, hkv, d),
+           "v": _randn(5, B, hkv, d)}
+    q, k, v = (torch.empty_like(src[x]) for x in "qkv")
+    cu = [0, 1, 4]
+    step = torch.ones(B, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    out = {}
+
+    def steps():
+        table.zero_()                                  # a fill
+        table.copy_(src["table"])                      # copies
+        lens.copy_(src["lens"])
+        for x, y in ((q, "q"), (k, "k"), (v, "v")):
+            x.copy_(src[y])
+        lens.add_(step)                                # a kernel
+        q_rot, k_rot = s2.rope_append(q, k, v, kc, vc, table, lens)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            po, plse = s2.prompt_fwd(q_rot, k_rot, v, cu)
+            scaled = po.float() * 2                    # torch's own kernel behind ours
+        o, lse = s2.decode(q_rot, kc, vc, table, lens)
+        total = o.float().sum(-1)
+        torch.cuda.current_stream().wait_stream(side)
+        lens.zero_()                                   # behind the last kernel that reads it
+        q.fill_(float("nan"))
+        out.update(q_rot=q_rot, k_rot=k_rot, po=po, plse=plse, scaled=scaled, o=o, lse=lse, total=total)
+
+    def look():
+        _ok()
+        now = [600, 18, 1, 321]
+        _check_decode(out["q_rot"], kc, vc, rows, now, d ** -0.5, out["o"], out["lse"])
+        _near_bf16(out["k_rot"], _turn64(src["k"], torch.tensor(now, device="cuda") - 1, 10000.0, 1.0), 1.2e-5)
+        want, want_lse, mean_abs = _prompt64(out["q_rot"], out["k_rot"], src["v"], cu, d ** -0.5)
+        _near_bf16(out["po"], want, (BF16_STEP + 1e-5) * mean_abs)
+        assert float((out["plse"].double() - want_lse).abs().max()) <= 2e-5
+        assert torch.equal(out["scaled"], out["po"].float() * 2) and torch.equal(out["total"], out["o"].float().sum(-1))
+
+    for _ in range(3):
+        steps()
+    look()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(5):
+        for x in ("q_rot", "k_rot", "po", "plse", "o", "lse"):
+            out[x].fill_(7.0)
+        graph.replay()
+        graph.replay()
+        look()
