@@ -26,12 +26,13 @@
 // TB/s the products of 16 padded rows need about 100 TFLOP/s, far below what it reaches, and the
 // fragment of the scores is the fragment of P in the second product, in registers. Scores, maxima,
 // sums and outputs are fp32; P is rounded to bf16 for the tensor cores, to twice bf16 where the MMA's
-// rows have room (8 query rows and less).
+// rows have room (8 query rows and less: output error against 64 bits 0.0017, that of its own rounding; with
+// 16 rows 0.0023).
 //
-// Measured: 16 sequences of about 8k tokens, 32 kv heads, 2.0 GB: 305 to 320 us, 6.3 to 6.6 TB/s (of measured
-// copy bandwidth: 0.97 to 1.0). One sequence of 102400 tokens, 8 kv heads, 419 MB: 73 us; the stream itself
+// Measured: 16 sequences of about 8k tokens, 32 kv heads, 2.0 GB: 312 to 318 us, 6.4 to 6.5 TB/s (of measured
+// copy bandwidth: 0.97 to 0.99). One sequence of 102400 tokens, 8 kv heads, 419 MB: 73 us; the stream itself
 // runs at 7.3 TB/s, 2 us pass before the first copy is on its way, 3 before it is there, 4 at the ranges'
-// uneven ends and joins and 5 in the second kernel. 64 sequences of 1 to 32768 tokens, 662 MB: 110 to 115 us.
+// uneven ends and joins and 5 in the second kernel. 64 sequences of 1 to 32768 tokens, 662 MB: 110 to 114 us.
 // Tried: 12 warps two tiles deep and K and V copied in groups of their own (not faster), wider L2 fetches
 // (no change), a dry round at the start to warm the instruction caches (3 us slower).
 #pragma once
@@ -51,7 +52,9 @@ constexpr int kDecodeGap = 1;
 // of the two ways, 8 kv heads, d = 128 (whole / split, us): 256 tokens 6.7 / 7.6 (one sequence), 6.9 / 7.8 (4),
 // 7.3 / 10.3 (16); 512 tokens 8.7 / 7.7, 9.0 / 9.1, 9.3 / 12.6; 1024 tokens 13.4 / 8.2, 13.6 / 9.8, 14.0 / 17.3.
 // A whole segment saves the second launch's 3 us of host time too; a longer limit would leave a batch of one
-// long and many short sequences to one CTA.
+// long and many short sequences to one CTA. The host sees the table's width only, not the lengths: a table of more
+// than 512 tokens a sequence is split however short they are, and the rule loses where the figures above cross it
+// (one sequence of 512 tokens, 16 of 1024).
 constexpr int kDecodeWholeTokens = 512;
 constexpr int kDecodeMaxCtas = 148;       // the workspace has room for this many CTAs' partials
 constexpr int kDecodeJoinThreads = 256;

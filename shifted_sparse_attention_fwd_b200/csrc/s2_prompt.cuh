@@ -33,13 +33,15 @@
 // O and l are rescaled. The price is range: O's sums of weights up to 2^30 a tile times values stay finite for
 // |v| < 2^98 / tiles (against the running maximum: 2^128 / keys).
 //
-// Measured, in a loop: one prompt of 8192 tokens, 32 heads, d = 128: 0.55 ms, 1.0 PFLOP/s of visible work; 39k
-// tokens in two prompts, 64 / 8 heads: 1.09 PFLOP/s; 12 prompts of 1 to 4999 tokens, 32 heads: 0.263 ms, 0.85; 64 prompts of
-// 128 tokens, 32 heads: 49 us, 5.5 TB/s (there the loads' latency and the memory bound it, and what a short unit costs
-// in sequence: 200 prompts of 40, 109 us).
-// Tensor pipe and exponential unit are each a good half busy at 1.7 GHz: the GPU sits at its power cap (990 W),
-// and a pass over the 8192 tokens takes 0.54 J, of which the MMAs alone need 0.36 (the same launch with the
-// softmax left out) and cuBLAS 0.39 for as many flops: energy, not a pipe, bounds it. Scores are loaded 16
+// Measured, in a loop over three inputs: one prompt of 8192 tokens, 32 heads, d = 128: 0.556 ms, 0.99 PFLOP/s of visible
+// work; 39k tokens in two prompts, 64 / 8 heads: 11.3 to 11.7 ms, 1.07 to 1.11; 12 prompts of 1 to 4999 tokens, 32 heads:
+// 0.267 ms, 0.84; 64 prompts of 128 tokens, 32 heads: 49 us, 5.5 TB/s (there the loads' latency and the memory bound it,
+// and what a short unit costs in sequence: 200 prompts of 40, 109 us).
+// What bounds it: tensor pipe and exponential unit are each 53 % busy, counted in their own cycles. One tile's step is a
+// chain, S product, pass, all of P stored, PV product, next S into the same columns, of some 3500 cycles, where the two
+// tiles' products take 2048 to 2750 and their exponentials 2048. In a loop the GPU sits at its power cap besides (990 W,
+// 1.7 GHz, 0.54 J a pass over the 8192 tokens; the MMAs alone, the same launch with the softmax left out, 0.36 J); a call
+// on its own, which the cap does not reach, takes 0.50 ms. Scores are loaded 16
 // columns at a time so that nothing spills (164 registers; 32 at a time: 4 % slower). Tried without gain: key
 // tiles of 64 with two score buffers per query tile (N = 64 MMAs: 0.79 ms), a warpgroup of its own for the
 // epilogue (128 registers a thread at launch spill the softmax: 0.79 ms), turns taken by the MMA issuers
@@ -261,7 +263,8 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[16]) {
 #undef S2_U8
 
 // 16 scores of a row: P = exp2(c s - m) as bf16 pairs into pk, the sums into acc. Scores behind column
-// `lim` are masked.
+// `lim` are masked. P is rounded to the tensor cores' 8 bits, as in the training forward (the sums are of the fp32
+// values): output error against 64 bits 0.0020, with fp32 weights it would be that of its own rounding, 0.0016.
 template <bool kMask>
 __device__ __forceinline__ void softmax16(const uint32_t (&r)[16], int lim, uint64_t c2, uint64_t nm2,
                                           uint32_t* pk, uint64_t (&acc)[2]) {
