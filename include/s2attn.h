@@ -420,12 +420,12 @@ S2ATTN_API size_t s2attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
  * of sequence b (the new token's key and value among them, appended before), q, o bf16 [B, Hq, d],
  * lse fp32 [B, Hq] (natural log; may be NULL). Query head h reads kv head h / (Hq / Hkv); any
  * group size. q must be turned already. A sequence of length 0 gives o = 0 and lse = -inf.
- * Cache rows past a sequence's length are never used, whatever they hold; infinite values that are seen
- * give infinite results. Finite values below 2^120 / cache_lens[b] never overflow the sums. The same inputs
- * give the same bits. `strides`: NULL or {q, o batch strides, k_cache sp, st, v_cache sp, st}. Calls that
- * may run at the same time need a workspace each. Two launches, of which the second one joins what was
- * split, or one where nothing is (block tables of up to 512 tokens a sequence and few sequences);
- * asynchronous on `stream`; allocates nothing.
+ * Cache rows past a sequence's length are never used, whatever they hold. An infinite value that is seen
+ * gives an infinite result (NaN where its weight underflows fp32 to 0). Finite values below 2^120 /
+ * cache_lens[b] never overflow the sums. The same inputs give the same bits. `strides`: NULL or {q, o
+ * batch strides, k_cache sp, st, v_cache sp, st}. Calls that may run at the same time need a workspace
+ * each. Two launches, of which the second one joins what was split, or one where nothing is (block tables
+ * of up to 512 tokens a sequence and few sequences); asynchronous on `stream`; allocates nothing.
  */
 S2ATTN_API s2attn_status s2attn_decode(const void* q, const void* k_cache, const void* v_cache,
                                        const int* block_table, const int* cache_lens, void* o,

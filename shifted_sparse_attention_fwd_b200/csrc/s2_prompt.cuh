@@ -37,7 +37,7 @@
 // work; 39k tokens in two prompts, 64 / 8 heads: 11.3 to 11.7 ms, 1.07 to 1.11; 12 prompts of 1 to 4999 tokens, 32 heads:
 // 0.267 ms, 0.84; 64 prompts of 128 tokens, 32 heads: 49 us, 5.5 TB/s (there the loads' latency and the memory bound it,
 // and what a short unit costs in sequence: 200 prompts of 40, 109 us).
-// What bounds it: tensor pipe and exponential unit are each 53 % busy, counted in their own cycles. One tile's step is a
+// What bounds it: tensor pipe and exponential unit are each 55 % busy, counted in their own cycles. One tile's step is a
 // chain, S product, pass, all of P stored, PV product, next S into the same columns, of some 3500 cycles, where the two
 // tiles' products take 2048 to 2750 and their exponentials 2048. In a loop the GPU sits at its power cap besides (990 W,
 // 1.7 GHz, 0.54 J a pass over the 8192 tokens; the MMAs alone, the same launch with the softmax left out, 0.36 J); a call
@@ -185,9 +185,9 @@ __device__ __forceinline__ uint32_t bf16x2_finite_part(uint32_t w) {
 
 // Adds to the stored rows of O of query tile t the infinities and NaN of the value rows they see in the unit's
 // diagonal tiles that were found to hold some (weights are positive: inf stays inf). One warp: a lane has D / 32
-// columns (pairs 64 apart), whose sum over the value rows runs along with the query rows, eight rows' loads in flight. Two full tiles
-// take some 40 us more, however many values are not finite (8192 tokens, 32 heads, nothing but NaN: 0.84 ms, 0.50
-// with finite values).
+// columns (pairs 64 apart), whose sum over the value rows runs along with the query rows, eight rows' loads in
+// flight. Two full tiles take some 40 us more, however many values are not finite (8192 tokens, 32 heads, nothing
+// but NaN: 0.84 ms, 0.50 with finite values).
 template <int D>
 __device__ __noinline__ void prompt_add_not_finite(const PromptParams& p, const PromptUnit& u, int bad, int t, int lane) {
   constexpr int kPer = D / 32, kWords = kPer / 2, kAhead = 8;
