@@ -1,6 +1,7 @@
 """The serving operators on the GPU where a call is unusual. Tolerances as derived in test_gpu_serve.py, whose
 helpers are used."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -415,3 +416,85 @@ def test_captured_steps_between_copies_fills_and_other_streams():
         graph.replay()
         graph.replay()
         look()
+
+
+# ------------------------------------------------------------------------------------------
+# the largest sizes
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [1 << 20, (1 << 27) + 5, (1 << 31) - 200])
+@pytest.mark.parametrize("hq", [1, 9])
+def test_decode_of_lengths_up_to_the_limit(n, hq):
+    """A table whose entries all name one page, so that the tokens repeat: the result is that of the repeated
+    tokens, each with its count, at any length that the table can hold."""
+    d = 64
+    # the largest pages with which the table stays within the library's limit of 2^31 - 129 tokens
+    page = next(x for x in range(1 << 20, 0, -1) if -(-n // x) * x <= (1 << 31) - 129)
+    width = -(-n // page)
+    kc, vc = _randn(1, 2, page, 1, d), _randn(2, 2, page, 1, d)
+    q = _randn(3, 2, hq, d)
+    table = torch.ones(2, width, dtype=torch.int32, device="cuda")
+    lens = [n, 3]
+    o, lse = s2.decode(q, kc, vc, table, _ints(lens))
+    _ok()
+    # token t of the page is seen n // page times, those before n % page once more
+    for b, m in enumerate(lens):
+        count = torch.full((page,), m // page, dtype=torch.float64, device="cuda")
+        count[:m % page] += 1
+        k, v = kc[1, :, 0].double(), vc[1, :, 0].double()
+        for h in range(hq):
+            s = (k @ q[b, h].double()) * d ** -0.5
+            want_lse = torch.logsumexp(s + count.log(), 0)
+            p = torch.exp(s - want_lse) * count
+            # fp32 sums of up to 2^31 terms: in 16-token steps, joined over 8 warps of 148 CTAs; one chain adds at
+            # most 2^31 / (1184 * 16) = 2^16.8 terms, each off by 2^-24 of the sum, in random directions and at
+            # worst all in one: 2^-7.2 of the weights' sum, o and l alike
+            chain = m / (1184 * 16) * 2.0 ** -24
+            _near_bf16(o[b, h], p @ v, (BF16_STEP + 1e-5 + 2 * chain) * (p @ v.abs()))
+            assert abs(float(lse[b, h]) - float(want_lse)) <= 2e-5 + chain
+
+
+def test_append_at_positions_up_to_the_limit():
+    d, page, hkv = 64, 1 << 16, 1
+    kc, vc = _randn(1, 2, page, hkv, d), _randn(2, 2, page, hkv, d)
+    width = ((1 << 31) - 129) // page
+    pos = [width * page - 1, width * page - 2, (1 << 30) + 12345]
+    table = torch.zeros(3, width, dtype=torch.int32, device="cuda")
+    k, v = _randn(3, 3, hkv, d), _randn(4, 3, hkv, d)
+    _, k_rot = s2.rope_append(None, k, v, kc, vc, table, _ints([p + 1 for p in pos]), pi_scale=0.3)
+    _ok()
+    # (angles of 2^29 rad in 64 bits are good to 2^-23 rad; the kernel's to 1e-6)
+    _near_bf16(k_rot, _turn64(k, torch.tensor(pos, device="cuda"), 10000.0, 0.3), 2.4e-5)
+    for i, p in enumerate(pos):
+        assert torch.equal(kc[0, p % page], k_rot[i]) and torch.equal(vc[0, p % page], v[i])
+    # one token more than the table holds
+    s2.rope_append(None, k, v, kc, vc, table, _ints([width * page + 1, 1, 1]))
+    torch.cuda.synchronize()
+    assert s2.s2attn_get_device_error() == (s2.S2ATTN_ERR_INVALID_ARG, (6 << 8) | 0x81)
+
+
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (2, 1, [270000, 700]),                             # more than 2048 tiles of 128 rows: two launches
+    (1, 1, [300, 530000]),                             # ... of 256 rows
+    (1, 1, [139] * 60000 + [1]),                       # 8.3 million rows, 118 launches
+])
+def test_prompts_of_more_tiles_than_a_launch_takes(hq, hkv, lens):
+    d = 64
+    cu = _cu(lens)
+    T = cu[-1]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(T, h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    o, lse = s2.prompt_fwd(q, k, v, torch.tensor(cu, dtype=torch.int32))
+    _ok()
+    assert o.isfinite().all() and lse.isfinite().all()
+    r = random.Random(7)
+    seqs = sorted({0, len(lens) - 1, len(lens) // 2} | {r.randrange(len(lens)) for _ in range(20)})
+    for s in seqs:
+        a, n = cu[s], lens[s]
+        for i in sorted({0, n - 1, n // 2, r.randrange(n), max(0, n - 129)}):
+            for h in range(hq):
+                kk, vv = k[a:a + i + 1, h * hkv // hq].double(), v[a:a + i + 1, h * hkv // hq].double()
+                sc = (kk @ q[a + i, h].double()) * d ** -0.5
+                want = torch.logsumexp(sc, 0)
+                p = torch.exp(sc - want)
+                _near_bf16(o[a + i, h], p @ vv, (BF16_STEP + 1e-5) * (p @ vv.abs()))
+                assert abs(float(lse[h, a + i]) - float(want)) <= 2e-5
